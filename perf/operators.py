@@ -367,7 +367,9 @@ def _run_plain(st):
         return _plain_route_grad(st)
     if op == "quant":
         x = st["x"].float()
-        s = x.abs().amax(1) / 127.0
+        top = x.abs().amax(1)
+        # a tensor of 127: torch multiplies by a rounded 1/127 for a number
+        s = top / torch.full_like(top, 127.0)
         s = torch.where(s > 0, s, 1.0)
         q = torch.round(x / s[:, None]).clamp_(-127, 127).to(torch.int8)
         if st["row_of"] is None:
