@@ -15,6 +15,7 @@
 #include <tuple>
 
 #include "../../include/mxgemm.h"
+#include "host.hpp"
 #include "kernels.hpp"
 #include "preshuffle.hpp"
 #include "quant.hpp"
@@ -41,20 +42,10 @@ FmtInfo fmt_info(int f) {
   }
 }
 
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
 // Largest operand extents the 32-bit in-kernel offsets support.
 constexpr int64_t MAX_ROW_BYTES = 1ll << 22;   // bytes of K per row (256 rows < 2^30)
-constexpr int64_t MAX_DIM = 1ll << 31;
 constexpr int64_t MAX_T_BYTES = 0x7FFFFFF0ll;   // a transposed operand, whole
 constexpr int64_t MAX_PSB_BYTES = (1ll << 32) - (1ll << 16);   // a preshuffled B, whole
-
-int launch_status() {
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? MXG_OK : MXG_ERR_HIP;
-}
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The persistent grouped kernels run GS_OCC workgroups per compute unit (74
 // KiB of LDS each with the group table: 64 x 64 tiles with two 128-K steps
@@ -70,21 +61,6 @@ constexpr int GS_OCC = 2;
 // one-step ring, whose two workgroups per unit took no less time per piece.
 constexpr int GROUPED_TAIL_ROUNDS = 2;
 
-// Compute units of the current device: the grid size of the persistent dense
-// kernel (one workgroup per compute unit).  Queried once per device.
-int cu_count() {
-  static int cache[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cache[dev] <= 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-      n = 256;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 }  // namespace
 
 // Kernel choice for a dense call from its static shapes: the persistent
@@ -98,8 +74,7 @@ int cu_count() {
 // of a load's latency).  Over that sweep the choice is the faster kernel
 // everywhere but at 2048 x 2048 x 256 (2.7 us slower).
 extern "C" int mxgemm_dense_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  (void)fmtA;
-  (void)fmtB;
+  if (fmtA == MXG_INT8 && fmtB == MXG_INT8) return int8_dense_variant(M, N, K);
   if (layout != MXG_NT || M <= 0 || N <= 0 || K <= 0) return MXG_DENSE_TILE256;
   const double cus = cu_count(), nst = (double)(K / 128);
   const double t256 = 6.0 + std::ceil((double)(cdiv(M, DBM) * cdiv(N, DBN)) / cus) * 1.3 * nst;
@@ -127,7 +102,7 @@ extern "C" int mxgemm_init(void) {
   if (hipFuncGetAttributes(&attr, (const void *)pick_dense_mx_a4(F_E4M3, MXG_NT, false, false)) != hipSuccess)
     return MXG_ERR_HIP;
   (void)cu_count();
-  return MXG_OK;
+  return int8_init();
 }
 
 extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,
@@ -135,7 +110,9 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
                     int64_t K) {
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  if (!fa.ok || !fb.ok) return MXG_ERR_INVALID_ARG;
+  const bool ia = fmtA == MXG_INT8, ib = (fmtB & ~MXG_PRESHUFFLED) == MXG_INT8;
+  if ((!fa.ok && !ia) || (!fb.ok && !ib)) return MXG_ERR_INVALID_ARG;
+  if (ia || ib) return int8_validate(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K);
   if (layout != MXG_NT && layout != MXG_NN && layout != MXG_TN) return MXG_ERR_INVALID_ARG;
   if (M < 0 || N < 0 || K < 0) return MXG_ERR_INVALID_ARG;
   if (M >= MAX_DIM || N >= MAX_DIM) return MXG_ERR_UNSUPPORTED;
@@ -197,6 +174,7 @@ __global__ void bias_act_fill_kernel(uint16_t *D, int64_t M, int64_t N, const ui
 
 int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
               void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, hipStream_t stream) {
+  if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, stream);
   const bool fuse = bias != nullptr || act != MXG_ACT_NONE;
   if (M == 0 || N == 0) return MXG_OK;
   if (K == 0) {
@@ -256,11 +234,14 @@ extern "C" int mxgemm_run(int fmtA, int fmtB, int layout, const void *A, const v
 extern "C" int mxgemm_validate_fused(int fmtA, int fmtB, int layout, const void *A, const void *sA,
                                      const void *B, const void *sB, const void *D, int64_t M, int64_t N,
                                      int64_t K, const void *bias, int activation) {
-  if (activation < MXG_ACT_NONE || activation > MXG_ACT_SILU) return MXG_ERR_INVALID_ARG;
+  // SwiGLU is built for the integer GEMM alone
+  const bool swiglu = activation == MXG_ACT_SWIGLU && fmtA == MXG_INT8;
+  if ((activation < MXG_ACT_NONE || activation > MXG_ACT_SILU) && !swiglu) return MXG_ERR_INVALID_ARG;
   const int v = mxgemm_validate(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K);
   if (v != MXG_OK) return v;
   if (bias == nullptr && activation == MXG_ACT_NONE) return MXG_OK;
   if (layout != MXG_NT) return MXG_ERR_UNSUPPORTED;
+  if (swiglu && N % 2 != 0) return MXG_ERR_UNSUPPORTED;
   if (bias != nullptr) {
     // the bias is staged by 4-byte DMAs of column pairs
     if (N % 2 != 0) return MXG_ERR_UNSUPPORTED;

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 OUT = os.path.join(PKG, "libmxgemm.so")
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "k_dense_mx4.hip", "k_dense_mx5.hip", "k_dense_tw4.hip", "k_dense_tw5.hip",
-           "k_dense_fp4.hip", "k_small.hip", "k_grouped.hip"]
+           "k_dense_fp4.hip", "k_small.hip", "k_grouped.hip", "k_int8.hip", "k_moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -15,12 +15,16 @@ LIB_PATH = os.path.join(_HERE, "libmxgemm.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_HIP = 0, -1, -2, -3, -4
 MXFP8_E4M3, MXFP8_E5M2, MXFP4_E2M1 = 0, 1, 4
 FP8_E4M3_TENSOR, FP8_E5M2_TENSOR = 16, 17
+INT8 = 32
+BF16, F32 = 64, 65
 PRESHUFFLED = 0x100
 NT, NN, TN = 0, 1, 2
 GROUPED_MAX_G = 1024
-GROUPED_STREAM64, GROUPED_TILED, GROUPED_STREAM128 = 0, 1, 2
-ACT_NONE, ACT_RELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3
-DENSE_TILE256, DENSE_TILE64 = 0, 1
+GROUPED_STREAM64, GROUPED_TILED, GROUPED_STREAM128, GROUPED_ROWS = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU_TANH, ACT_SILU, ACT_SWIGLU = 0, 1, 2, 3, 8
+DENSE_TILE256, DENSE_TILE64, DENSE_TILE128, DENSE_ROWS = 0, 1, 2, 3
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 EXPORTS = (
     "mxgemm_init", "mxgemm_status_string", "mxgemm_run", "mxgemm_validate",
@@ -34,6 +38,8 @@ EXPORTS = (
     "grouped_bf16_gemm_run", "grouped_bf16_gemm_validate", "grouped_bf16_gemm_variant",
     "grouped_bf16_preshuffle_b",
     "mxgemm_quantize_mx", "mxgemm_quantize_tensor", "grouped_fp8_quantize_act", "grouped_fp8_quantize_weight",
+    "grouped_int8_gemm_run", "grouped_int8_gemm_validate", "grouped_int8_gemm_variant", "mxgemm_quantize_int8",
+    "moe_route_workspace_bytes", "moe_route", "moe_route_backward", "moe_combine", "moe_combine_backward",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -100,6 +106,25 @@ _lib.grouped_fp8_quantize_weight.restype = _i
 _lib.grouped_fp8_quantize_weight.argtypes = [_i, _p, _p, _p, _i64, _i64, _p]
 _lib.grouped_fp8_quantize_act.restype = _i
 _lib.grouped_fp8_quantize_act.argtypes = [_i, _p, _p, _p, _p, _i64, _i64, _p]
+_f = ctypes.c_float
+_lib.grouped_int8_gemm_run.restype = _i
+_lib.grouped_int8_gemm_run.argtypes = [_i, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i, _p]
+_lib.grouped_int8_gemm_validate.restype = _i
+_lib.grouped_int8_gemm_validate.argtypes = [_i, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i]
+_lib.grouped_int8_gemm_variant.restype = _i
+_lib.grouped_int8_gemm_variant.argtypes = [_i, _i64, _i64, _i64]
+_lib.mxgemm_quantize_int8.restype = _i
+_lib.mxgemm_quantize_int8.argtypes = [_i, _p, _p, _p, _i64, _i64, _p, _i, _p]
+_lib.moe_route_workspace_bytes.restype = _i64
+_lib.moe_route_workspace_bytes.argtypes = [_i64, _i64]
+_lib.moe_route.restype = _i
+_lib.moe_route.argtypes = [_i, _p, _p, _p, _p, _i64, _i64, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p, _p, _i64, _p]
+_lib.moe_route_backward.restype = _i
+_lib.moe_route_backward.argtypes = [_i, _p, _p, _p, _p, _i64, _i64, _i, _i, _i, _f, _p]
+_lib.moe_combine.restype = _i
+_lib.moe_combine.argtypes = [_p, _p, _p, _p, _i64, _i, _i64, _i64, _p]
+_lib.moe_combine_backward.restype = _i
+_lib.moe_combine_backward.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i, _i64, _i64, _p]
 
 
 class MxgemmError(RuntimeError):
@@ -170,14 +195,15 @@ def validate(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K):
 
 
 def dense_variant(fmtA, fmtB, layout, M, N, K):
-    """DENSE_TILE256 or DENSE_TILE64: the kernel run / run_fused launch for
-    these shapes on the current device."""
+    """DENSE_TILE256 or DENSE_TILE64 (INT8 also DENSE_TILE128, DENSE_ROWS): the
+    kernel run / run_fused launch for these shapes on the current device."""
     return _lib.mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K)
 
 
 def run_fused(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias=None, activation=ACT_NONE,
               stream=None):
-    """D = act(sum_k a(m,k) b(n,k) + bias[n]) in BF16; bias: BF16 [N] or None."""
+    """D = act(sum_k a(m,k) b(n,k) + bias[n]) in BF16; bias: BF16 [N] or None.
+    ACT_SWIGLU (INT8 operands only): D is [M, N/2]."""
     _check(_lib.mxgemm_run_fused(fmtA, fmtB, layout, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(D),
                                  M, N, K, _ptr(bias), activation, _stream(stream)), "mxgemm_run_fused")
 
@@ -307,3 +333,71 @@ def grouped_quantize_weight(G, w, codes, w_scale, N, K, stream=None):
     """FP32 weights [G, N, K] -> E4M3 codes and FP32 128 x 128 block scales."""
     _check(_lib.grouped_fp8_quantize_weight(G, _ptr(w), _ptr(codes), _ptr(w_scale), N, K, _stream(stream)),
            "grouped_fp8_quantize_weight")
+
+
+def grouped_int8_run(G, m_sizes, XQ, x_scale, WQ, w_scale, D, totM, N, K, activation=ACT_NONE, stream=None):
+    """8-bit integer grouped GEMM: D[rows of g] = act(x_scale w_scale[g] XQ
+    WQ[g]^T); ACT_SWIGLU writes D [totM, N/2]; see include/mxgemm.h."""
+    _check(_lib.grouped_int8_gemm_run(G, _ptr(m_sizes), _ptr(XQ), _ptr(x_scale), _ptr(WQ), _ptr(w_scale),
+                                      _ptr(D), totM, N, K, activation, _stream(stream)), "grouped_int8_gemm_run")
+
+
+def grouped_int8_validate(G, m_sizes, XQ, x_scale, WQ, w_scale, D, totM, N, K, activation=ACT_NONE):
+    return _lib.grouped_int8_gemm_validate(G, _ptr(m_sizes), _ptr(XQ), _ptr(x_scale), _ptr(WQ), _ptr(w_scale),
+                                           _ptr(D), totM, N, K, activation)
+
+
+def grouped_int8_variant(G, totM, N, K):
+    """GROUPED_STREAM64, GROUPED_STREAM128, GROUPED_TILED or GROUPED_ROWS: the
+    kernel grouped_int8_run launches for these static shapes."""
+    return _lib.grouped_int8_gemm_variant(G, totM, N, K)
+
+
+def quantize_int8(dtype, x, codes, scales, T, K, row_of=None, topk=1, stream=None):
+    """Rows of x (dtype BF16 or F32) -> int8 codes and one FP32 scale per row;
+    with row_of [T, topk] into the experts' rows (see include/mxgemm.h)."""
+    _check(_lib.mxgemm_quantize_int8(dtype, _ptr(x), _ptr(codes), _ptr(scales), T, K, _ptr(row_of), topk,
+                                     _stream(stream)), "mxgemm_quantize_int8")
+
+
+def moe_route_workspace_bytes(T, E):
+    return _lib.moe_route_workspace_bytes(T, E)
+
+
+def moe_route(dtype, logits, bias, ids, weights, T, E, topk, score=MOE_SOFTMAX, n_group=1, topk_group=1,
+              group_score=MOE_GROUP_MAX, renormalize=True, scale=1.0, m_sizes=None, row_of=None, slot_of=None,
+              workspace=None, stream=None):
+    """Each token's topk experts (ids, -1: none) and their weights and, with
+    m_sizes, row_of and slot_of, the order of the experts' rows; workspace:
+    a device tensor of moe_route_workspace_bytes(T, E) bytes or more (see
+    include/mxgemm.h)."""
+    if workspace is None:
+        nbytes = 0
+    elif isinstance(workspace, int):
+        nbytes = _lib.moe_route_workspace_bytes(T, E)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    ws = _ptr(workspace) if nbytes > 0 else None
+    _check(_lib.moe_route(dtype, _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), T, E, topk, score, n_group,
+                          topk_group, group_score, int(bool(renormalize)), scale, _ptr(m_sizes), _ptr(row_of),
+                          _ptr(slot_of), ws, nbytes, _stream(stream)), "moe_route")
+
+
+def moe_route_backward(dtype, logits, ids, grad, dlogits, T, E, topk, score=MOE_SOFTMAX, renormalize=True,
+                       scale=1.0, stream=None):
+    """Gradient of moe_route's weights (grad [T, topk]) with respect to the
+    logits, written in full to dlogits [T, E]."""
+    _check(_lib.moe_route_backward(dtype, _ptr(logits), _ptr(ids), _ptr(grad), _ptr(dlogits), T, E, topk, score,
+                                   int(bool(renormalize)), scale, _stream(stream)), "moe_route_backward")
+
+
+def moe_combine(y, w, row_of, out, T, topk, N, rows, stream=None):
+    """out[t] = sum_j w[t,j] y[row_of[t,j]] (BF16 rows, FP32 sums)."""
+    _check(_lib.moe_combine(_ptr(y), _ptr(w), _ptr(row_of), _ptr(out), T, topk, N, rows, _stream(stream)),
+           "moe_combine")
+
+
+def moe_combine_backward(dout, y, w, row_of, dy, dw, T, topk, N, rows, stream=None):
+    """Gradient of moe_combine: dy (the rows that row_of names) and dw [T, topk]."""
+    _check(_lib.moe_combine_backward(_ptr(dout), _ptr(y), _ptr(w), _ptr(row_of), _ptr(dy), _ptr(dw), T, topk, N,
+                                     rows, _stream(stream)), "moe_combine_backward")

@@ -1,7 +1,9 @@
 /*
  * mxgemm.h -- C ABI of the MI355X (gfx950) block-scaled GEMM library.
  *
- * One operation, three scale families:
+ * One operation, three scale families (a fourth, 8-bit integers with scales
+ * for each row, and the operators of a mixture-of-experts layer around it, at
+ * the end of this file):
  *
  *     D[m,n] = sum_k a(m,k) * b(n,k)        (FP32 accumulation, BF16 output)
  *
@@ -24,11 +26,13 @@
  *
  * Conventions for every entry point:
  *  - All data pointers are DEVICE pointers owned by the caller.  The library
- *    never allocates, frees or retains caller memory and uses no workspace.
+ *    never allocates, frees or retains caller memory and uses no workspace
+ *    (moe_route alone takes one from the caller; see there).
  *  - Calls are stream-ordered and asynchronous: exactly one kernel is
  *    enqueued on `stream` (0 = the null stream) per successful call, with
  *    two exceptions: mxgemm_quantize_tensor enqueues four (its scale output
- *    serves as the amax word between them; see there), and
+ *    serves as the amax word between them; see there), moe_route at most
+ *    two (see there), and
  *    grouped_fp8_gemm_run and grouped_bf16_gemm_run enqueue two when they
  *    run MXG_GROUPED_TILED on more 256 x 256 tiles than the device has
  *    compute units (see grouped_fp8_gemm_variant).  The tuning call grouped_fp8_gemm_autotune
@@ -73,7 +77,9 @@ enum {
   MXG_MXFP4_E2M1 = 4,         /* E2M1 codes two per byte (element 2j in bits 3:0,
                                  2j+1 in bits 7:4) + E8M0 scale per 32 along K  */
   MXG_FP8_E4M3_TENSOR = 16,   /* E4M3 codes + one FP32 dequant multiplier        */
-  MXG_FP8_E5M2_TENSOR = 17    /* E5M2 codes + one FP32 dequant multiplier        */
+  MXG_FP8_E5M2_TENSOR = 17,   /* E5M2 codes + one FP32 dequant multiplier        */
+  MXG_INT8 = 32               /* signed 8-bit codes + one FP32 scale per row (A:
+                                 per m, a token; B: per n, a channel); NT only   */
 };
 
 /* OR into fmtB: B's codes (and, for MX, sB) were produced by
@@ -108,7 +114,8 @@ const char *mxgemm_status_string(int status);
  *
  * fmtA, fmtB  operand formats (MXG_MXFP8_*, MXG_MXFP4_E2M1, MXG_FP8_*_TENSOR);
  *             both MX or both tensor-wise; E2M1 only with E2M1.  fmtB may
- *             carry MXG_PRESHUFFLED (NT only).
+ *             carry MXG_PRESHUFFLED (NT only).  MXG_INT8 only with itself:
+ *             its own rules at "8-bit integers" below.
  * layout      MXG_NT, MXG_NN or MXG_TN (see the header comment).
  * A, B        codes: uint8, row-major in the layout's storage shape.  E2M1 is
  *             packed two per byte along the contiguous dimension (element
@@ -146,7 +153,10 @@ int mxgemm_run(int fmtA, int fmtB, int layout,
  * compute the same function with the same per-element sequence of
  * matrix-core instructions, so their outputs are identical.  Never fails.
  */
-enum { MXG_DENSE_TILE256 = 0, MXG_DENSE_TILE64 = 1 };
+/* MXG_INT8 has two more: MXG_DENSE_TILE128 (128 x 128 tiles) and
+ * MXG_DENSE_ROWS (few rows: the weights stream through registers); its sums
+ * are exact, so all four give the same bits. */
+enum { MXG_DENSE_TILE256 = 0, MXG_DENSE_TILE64 = 1, MXG_DENSE_TILE128 = 2, MXG_DENSE_ROWS = 3 };
 int mxgemm_dense_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K);
 
 /* Host-only check of mxgemm_run's arguments (no device call), for the
@@ -180,7 +190,8 @@ int mxgemm_validate(int fmtA, int fmtB, int layout,
  * bias == NULL and MXG_ACT_NONE the call is mxgemm_run.  K == 0 writes
  * act(bias[n]).
  */
-enum { MXG_ACT_NONE = 0, MXG_ACT_RELU = 1, MXG_ACT_GELU_TANH = 2, MXG_ACT_SILU = 3 };
+enum { MXG_ACT_NONE = 0, MXG_ACT_RELU = 1, MXG_ACT_GELU_TANH = 2, MXG_ACT_SILU = 3,
+       MXG_ACT_SWIGLU = 8 /* 8-bit integer GEMM only; see there */ };
 int mxgemm_run_fused(int fmtA, int fmtB, int layout,
                      const void *A, const void *sA, const void *B, const void *sB,
                      void *D, int64_t M, int64_t N, int64_t K,
@@ -501,6 +512,161 @@ int grouped_fp8_quantize_weight(int G, const float *w, void *codes, float *w_sca
  * (unknown fmt, iters < 0, null clk), MXG_ERR_MISALIGNED.
  */
 int mxgemm_mfma_ceiling(int fmt, int64_t iters, void *clk, hipStream_t stream);
+
+/*
+ * 8-bit integers (MXG_INT8): D[m,n] = act( sA[m] sB[n] sum_k A[m,k] B[n,k]
+ * + bias[n] ), through mxgemm_run, mxgemm_run_fused and their _validate.
+ *
+ * A, B    signed 8-bit [M,K] and [N,K] (MXG_NT only, not preshuffled),
+ *         16-byte aligned; every code from -128 to 127 is allowed.
+ * sA, sB  FP32 [M] and [N]: the scale of each row of A (token) and of each
+ *         row of B (channel), 4-byte aligned.
+ * The sum is exact in 32-bit integers, which bounds K: a multiple of 16, at
+ * most 131056 (128 * 128 * K < 2^31).  It is rounded to FP32, multiplied by
+ * sA[m], then by sB[n], the bias is added and the activation applied in
+ * FP32, and the result is rounded once to BF16.
+ * MXG_ACT_SWIGLU: columns 2j (gate) and 2j + 1 (up) of the product give
+ * D[m,j] = z[2j] / (1 + e^-z[2j]) * z[2j+1]; D is [M, N/2] and N even.
+ * M, N any size (bias and SwiGLU: N even), D 16-byte aligned.
+ * Errors as mxgemm_run_fused; MXG_INT8 with another format, another layout
+ * or MXG_PRESHUFFLED is MXG_ERR_UNSUPPORTED.
+ *
+ * grouped_int8_gemm_run -- the same product for each group of rows (expert):
+ * D[r,n] = act( x_scale[r] w_scale[g,n] sum_k XQ[r,k] WQ[g,n,k] ) for the
+ * rows r of group g.
+ * G, m_sizes  as grouped_fp8_gemm_run (the device's m_sizes are never read
+ *         by the host; groups are cut at totM; an empty group owns no rows;
+ *         rows of D in no group are left untouched).
+ * XQ      signed 8-bit [totM, K]; x_scale FP32 [totM] (not the block layout
+ *         of the FP8 GEMM).
+ * WQ      signed 8-bit [G, N, K]; w_scale FP32 [G, N].
+ * D       BF16 [totM, N], with MXG_ACT_SWIGLU [totM, N/2].
+ * K as above, N any size (SwiGLU: even).  K == 0 writes act(0) = 0 to every
+ * row of every group.  grouped_int8_gemm_variant names the kernel
+ * (MXG_GROUPED_*) for these static shapes: MXG_GROUPED_ROWS streams the
+ * weights through registers, for few rows per group; the choice never
+ * depends on m_sizes' contents and all kernels give the same bits.
+ */
+enum { MXG_GROUPED_ROWS = 3 };
+int grouped_int8_gemm_run(int G, const int64_t *m_sizes, const void *XQ, const float *x_scale,
+                          const void *WQ, const float *w_scale, void *D, int64_t totM, int64_t N,
+                          int64_t K, int activation, hipStream_t stream);
+int grouped_int8_gemm_validate(int G, const int64_t *m_sizes, const void *XQ, const float *x_scale,
+                               const void *WQ, const float *w_scale, const void *D, int64_t totM,
+                               int64_t N, int64_t K, int activation);
+int grouped_int8_gemm_variant(int G, int64_t totM, int64_t N, int64_t K);
+
+/* Element types of the operators below. */
+enum { MXG_BF16 = 64, MXG_F32 = 65 };
+
+/*
+ * mxgemm_quantize_int8 -- rows of activations (or weights) -> signed 8-bit
+ * codes and one FP32 scale per row, the operands of the MXG_INT8 GEMMs,
+ * optionally in the order of the experts' rows.
+ *
+ * dtype   MXG_BF16 or MXG_F32: x is [T, K] of it, row-major, 16-byte aligned.
+ * Per row: s = max |x| / 127 as an FP32 quotient (1.0 where that is zero: an
+ * all-zero row, or one so small that the quotient underflows), code = the
+ * nearest integer to the FP32 quotient x / s, ties to even, cut to +-127.
+ * Inputs must be finite.
+ * row_of  NULL (topk 1): row t of codes and scales is row t of x.  Else
+ *         int32 [T, topk] as moe_route writes it: row t goes to the rows
+ *         row_of[t, 0 .. topk-1]; entries outside [0, T topk) are skipped,
+ *         and output rows that no entry names are left untouched.
+ * codes   int8 [T topk, K], 16-byte aligned; scales FP32 [T topk].
+ * K a multiple of 16, at most 131056; topk 1 .. 64 (MXG_ERR_UNSUPPORTED).
+ * T or K = 0: no-op.
+ */
+int mxgemm_quantize_int8(int dtype, const void *x, void *codes, float *scales, int64_t T, int64_t K,
+                         const int32_t *row_of, int topk, hipStream_t stream);
+
+/*
+ * moe_route -- the router of a mixture-of-experts layer: each token's topk
+ * experts, their weights, and the order of the experts' rows.
+ *
+ * dtype   MXG_BF16 or MXG_F32: logits [T, E] of it, row-major.  A logit of
+ *         -inf (or NaN) makes that expert unavailable to that token.
+ * score   MXG_MOE_SOFTMAX: s = softmax of the token's available logits;
+ *         MXG_MOE_SIGMOID: s = 1 / (1 + e^-l).
+ * bias    NULL or FP32 [E], finite, for balance: it is added to the scores
+ *         to choose the experts and takes no part in the weights.
+ * n_group, topk_group, group_score   with n_group > 1 the experts form
+ *         n_group equal groups of consecutive ones, and only those of the
+ *         token's topk_group best groups can be chosen.  A group's score is
+ *         its largest choice value (MXG_MOE_GROUP_MAX) or the sum of its two
+ *         largest s + bias (MXG_MOE_GROUP_TOP2); a group with no available
+ *         expert comes last and gives none.
+ * The choice value is l without a bias and s + bias with one, the latter in
+ * 64 bits; experts (and groups) are ordered by falling value, ties by rising
+ * index.
+ * ids     int32 [T, topk], best first; -1 past the last available expert (a
+ *         token with none gets -1 throughout).
+ * weights FP32 [T, topk]: s of the chosen experts, with `renormalize`
+ *         divided by their sum (formed so that scores too small for FP32
+ *         still share the weight), times `scale`; 0 beside an id of -1.
+ * The order of the experts' rows, all three or none (NULL): the chosen
+ * (token, slot) pairs sorted by expert, then by token.
+ *   m_sizes int64 [E]: rows of each expert (grouped_*_gemm_run's m_sizes);
+ *   row_of  int32 [T, topk]: the row of each slot, -1 beside an id of -1;
+ *   slot_of int32 [T topk]: the slot (t topk + j) of each row, -1 past the
+ *           last row.
+ * workspace, workspace_bytes   16-byte aligned device memory of at least
+ *         moe_route_workspace_bytes(T, E) bytes for the calls with the three
+ *         maps (else unused); it is free for other use once the call's work
+ *         is done.
+ * At most two kernels are enqueued.  E <= 1024, topk <= min(E, 32),
+ * n_group <= 64, n_group divides E, 1 <= topk_group <= n_group, T <= 2^24
+ * (MXG_ERR_UNSUPPORTED); an unknown enum, null pointer, negative size or small
+ * workspace is MXG_ERR_INVALID_ARG; logits 16-byte aligned.  T = 0 is a no-op, except that
+ * m_sizes is set to zero.
+ */
+enum { MXG_MOE_SOFTMAX = 0, MXG_MOE_SIGMOID = 1 };
+enum { MXG_MOE_GROUP_MAX = 0, MXG_MOE_GROUP_TOP2 = 1 };
+int64_t moe_route_workspace_bytes(int64_t T, int64_t E);
+int moe_route(int dtype, const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T,
+              int64_t E, int topk, int score, int n_group, int topk_group, int group_score, int renormalize,
+              float scale, int64_t *m_sizes, int32_t *row_of, int32_t *slot_of, void *workspace,
+              int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route's weights with respect to
+ * the logits (the choice itself has none, nor has the bias).
+ *
+ * ids, grad  int32 and FP32 [T, topk]: the chosen experts (those outside
+ *         [0, E) are skipped; each expert at most once per token) and the
+ *         gradient of their weights.
+ * dlogits [T, E] of dtype, written in full; with c = scale * grad and w the
+ *         chosen scores divided by their sum:
+ *   softmax:              s_e (c_e - sum_j c_j s_j)      (c_e = 0 if not chosen)
+ *   softmax, renormalize: w_e (c_e - sum_j c_j w_j)
+ *   sigmoid:              c_e s_e (1 - s_e)
+ *   sigmoid, renormalize: w_e (1 - s_e) (c_e - sum_j c_j w_j)
+ * (the last two lines with renormalize are 0 for experts not chosen).  An
+ * unavailable expert's gradient is 0.  Sums are FP32, rounded once to dtype.
+ * Limits and errors as moe_route.
+ */
+int moe_route_backward(int dtype, const void *logits, const int32_t *ids, const float *grad, void *dlogits,
+                       int64_t T, int64_t E, int topk, int score, int renormalize, float scale,
+                       hipStream_t stream);
+
+/*
+ * moe_combine -- the experts' rows back to their tokens:
+ * out[t] = sum_j w[t,j] y[row_of[t,j]], j rising, FP32 sums, one rounding.
+ *
+ * y       BF16 [rows, N]; w FP32 [T, topk]; row_of int32 [T, topk], entries
+ *         outside [0, rows) are skipped (a token of none gets zeros).
+ * out     BF16 [T, N].  All row-major; y and out 16-byte aligned.
+ * topk 1 .. 64 (MXG_ERR_UNSUPPORTED).  T or N = 0: no-op.
+ *
+ * moe_combine_backward -- its gradient: dy[row_of[t,j]] = w[t,j] dout[t]
+ * (BF16) and dw[t,j] = sum_n y[row_of[t,j], n] dout[t, n] (FP32 sums; 0 for a
+ * skipped entry, and for N = 0).  dy rows that no entry names are left
+ * untouched; each row may be named once.
+ */
+int moe_combine(const void *y, const float *w, const int32_t *row_of, void *out, int64_t T, int topk,
+                int64_t N, int64_t rows, hipStream_t stream);
+int moe_combine_backward(const void *dout, const void *y, const float *w, const int32_t *row_of, void *dy,
+                         float *dw, int64_t T, int topk, int64_t N, int64_t rows, hipStream_t stream);
 
 #ifdef __cplusplus
 }
