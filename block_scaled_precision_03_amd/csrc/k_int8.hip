@@ -46,10 +46,12 @@ int launch(Int8Args &a, hipStream_t stream) {
   if (tiles > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
   if (tiled) {
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, cu_count());
-    if (a.act == ACT_SWIGLU)
-      hipLaunchKernelGGL((int8_tiled_kernel<true>), dim3(grid), dim3(DNW8 * 64), 0, stream, a);
-    else
-      hipLaunchKernelGGL((int8_tiled_kernel<false>), dim3(grid), dim3(DNW8 * 64), 0, stream, a);
+    void (*fn)(Int8Args) = a.act == ACT_SWIGLU      ? int8_tiled_kernel<ACT_SWIGLU>
+                           : a.act == ACT_RELU      ? int8_tiled_kernel<ACT_RELU>
+                           : a.act == ACT_GELU_TANH ? int8_tiled_kernel<ACT_GELU_TANH>
+                           : a.act == ACT_SILU      ? int8_tiled_kernel<ACT_SILU>
+                                                    : int8_tiled_kernel<ACT_NONE>;
+    hipLaunchKernelGGL(fn, dim3(grid), dim3(DNW8 * 64), 0, stream, a);
   } else {
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 2ll * cu_count());
     if (BT == 64)
@@ -107,7 +109,7 @@ int int8_run(const void *A, const void *sA, const void *B, const void *sB, void 
 
 int int8_init() {
   hipFuncAttributes attr;
-  return hipFuncGetAttributes(&attr, (const void *)int8_tiled_kernel<false>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
+  return hipFuncGetAttributes(&attr, (const void *)int8_tiled_kernel<ACT_NONE>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
 }
 
 }  // namespace mxg

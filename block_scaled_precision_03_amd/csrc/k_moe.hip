@@ -134,8 +134,9 @@ extern "C" int moe_route(int dtype, const void *logits, const float *bias, int32
   if (!fits) return MXG_ERR_UNSUPPORTED;
   a.lpg = s.lpg;
   a.per = s.per;
-  // one block: up to 16 waves, so that its tokens run at once
-  const int threads = one ? (int)std::min<int64_t>(1024, std::max<int64_t>(256, cdiv(T * s.lpt, 64) * 64)) : 256;
+  // up to 16 waves, so that a block's 64 tokens run at once
+  const int64_t per_block = std::min<int64_t>(T, ROUTE_TG);
+  const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(256, cdiv(per_block * s.lpt, 64) * 64));
   route_fn fn = dtype == MXG_BF16 ? pick_route<uint16_t>(s, maps, one) : pick_route<float>(s, maps, one);
   hipLaunchKernelGGL(fn, dim3((unsigned)a.nblk), dim3((unsigned)threads), 0, stream, a);
   if (maps && !one) hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)a.nblk), dim3(256), 0, stream, a);
