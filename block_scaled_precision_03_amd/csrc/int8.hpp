@@ -67,46 +67,43 @@ __device__ inline void int8_group_table(const Int8Args &p, GroupTable &gt, int l
   }
 }
 
+__device__ inline v4f unpack_bf16x4(const v2i &w) {
+  return (v4f){__uint_as_float((uint32_t)w.x << 16), __uint_as_float((uint32_t)w.x & 0xFFFF0000u),
+               __uint_as_float((uint32_t)w.y << 16), __uint_as_float((uint32_t)w.y & 0xFFFF0000u)};
+}
+
 // Four consecutive output columns (SwiGLU: two) of one row, from column col
-// (a multiple of 4) of the product, by the widest store that the row pitch
-// allows.  v is the finished result.
+// (a multiple of 4) of the product, in one store at whatever alignment an odd
+// row pitch leaves (the hardware takes any).  v is the finished result.
 __device__ inline void int8_store4(const Int8Args &p, int act, int64_t row, int64_t col, const v4f &v) {
   if (act == ACT_SWIGLU) {
     const int64_t oc = col >> 1;
     uint16_t *dst = p.D + row * p.No + oc;
     const uint32_t u = swiglu_pack(v);
-    if ((p.No & 1) == 0) {
-      if (oc < p.No) *(uint32_t *)dst = u;
-    } else {
-      if (oc < p.No) dst[0] = (uint16_t)u;
-      if (oc + 1 < p.No) dst[1] = (uint16_t)(u >> 16);
-    }
+    if (oc + 2 <= p.No) __builtin_memcpy(dst, &u, 4);
+    else if (oc < p.No) dst[0] = (uint16_t)u;
     return;
   }
   uint16_t *dst = p.D + row * p.No + col;
-  const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
-  if ((p.No & 3) == 0) {
-    if (col < p.No) *(v2i *)dst = (v2i){(int)lo, (int)hi};
-  } else if ((p.No & 1) == 0) {
-    if (col < p.No) ((uint32_t *)dst)[0] = lo;
-    if (col + 2 < p.No) ((uint32_t *)dst)[1] = hi;
+  const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+  if (col + 4 <= p.No) {
+    __builtin_memcpy(dst, u, 8);
   } else {
-    if (col < p.No) dst[0] = (uint16_t)lo;
-    if (col + 1 < p.No) dst[1] = (uint16_t)(lo >> 16);
-    if (col + 2 < p.No) dst[2] = (uint16_t)hi;
-    if (col + 3 < p.No) dst[3] = (uint16_t)(hi >> 16);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (col + k < p.No) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
   }
 }
 
-// The FP32 channel scales and biases of four consecutive columns from
-// memory (edge columns read 0; their results are never stored).
-__device__ inline void int8_columns(const Int8Args &p, int g, int64_t col, v4f &sb, v4f &bias) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const bool in = col + k < p.N;
-    sb[k] = in ? p.sB[(int64_t)g * p.N + col + k] : 0.0f;
-    bias[k] = in && p.bias ? __uint_as_float((uint32_t)p.bias[col + k] << 16) : 0.0f;
-  }
+// The FP32 channel scales and biases of the four consecutive columns n0 + c
+// .. from memory (n0 uniform; columns past N read 0, their results are never
+// stored), by range-checked loads: with a branch per column their latencies
+// add up.
+__device__ inline void int8_columns(const Int8Args &p, int g, int64_t n0, int c, v4f &sb, v4f &bias) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.sB + (int64_t)g * p.N + n0, clamp_records(4 * (p.N - n0)));
+  const __amdgpu_buffer_rsrc_t rb = p.bias ? make_rsrc(p.bias + n0, clamp_records(2 * (p.N - n0))) : make_rsrc(p.D, 0);
+  sb = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, 4 * c, 0, 0));
+  bias = unpack_bf16x4(__builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rb, 2 * c, 0, 0)));
 }
 
 // ---------------------------------------------------------------------------
@@ -218,8 +215,9 @@ struct Int8Loop {
     e.lim = t.lim;
     e.slot = t.slot;
     e.on = on;
-    // 16-byte stores through a range-checked 32-bit offset (see DenseLoop)
-    e.full = t.m0 + DBM <= t.lim && t.n0 + DBN <= p.N && (p.No & 7) == 0 && p.No <= (1 << 22);
+    // 16-byte stores through a range-checked 32-bit offset (see DenseLoop), at
+    // any alignment
+    e.full = t.m0 + DBM <= t.lim && t.n0 + DBN <= p.N && p.No <= (1 << 22);
     const int64_t org = t.m0 * p.No + (SWIGLU ? t.n0 / 2 : t.n0);
     e.rd = rsrc4(p.D + org, clamp_records(2 * (p.M * p.No - org)));
     e.rowstride = (uint32_t)(32 * p.No);
@@ -243,10 +241,7 @@ struct Int8Loop {
       const uint32_t o = (uint32_t)(c.wn * 64 + b * 16 + 4 * q);
       const v4i s = *(const lds_v4i *)(uintptr_t)(sc + SB_OFF + o * 4);
       const v2i w = *(const lds_v2i *)(uintptr_t)(sc + BIAS_OFF + o * 2);
-      const v4f sb = __builtin_bit_cast(v4f, s);
-      const v4f bias = {__uint_as_float((uint32_t)w.x << 16), __uint_as_float((uint32_t)w.x & 0xFFFF0000u),
-                        __uint_as_float((uint32_t)w.y << 16), __uint_as_float((uint32_t)w.y & 0xFFFF0000u)};
-      return int8_finish(row[b], sa, sb, bias, ACT);
+      return int8_finish(row[b], sa, __builtin_bit_cast(v4f, s), unpack_bf16x4(w), ACT);
     };
     if (e.full) {
       uint32_t rs = e.rowstride;
@@ -422,16 +417,29 @@ __global__ __launch_bounds__(DNW8 * 64, 1) void int8_tiled_kernel(Int8Args p) {
 }
 
 // ---------------------------------------------------------------------------
-// BM x BN tiles (64 x 64 or 128 x 128) on the streaming schedule of
-// grouped_stream_kernel: four waves in 2 x 2, a two-slot ring of stages of KS
-// K steps that runs across tile boundaries, two workgroups per compute unit,
-// tiles in XCD bands.  For outputs with too few 256 x 256 tiles to occupy the
-// device.
-template <int BM, int BN, int KS>
+// BM x BN tiles (64 x 64 or 128 x 128), for outputs with too few 256 x 256
+// tiles to occupy the device: four waves in 2 x 2, a ring of NS stages of KS K
+// steps that runs across tile boundaries, two workgroups per compute unit,
+// tiles in XCD bands.  Per K step a workgroup takes 0.36 us (64 x 64) or 0.8
+// us (128 x 128) where it has the compute unit alone, whatever the ring's
+// depth: with one wave per SIMD it is the ~100 instructions of a step, the
+// barrier and the latencies between them that count.  With two workgroups
+// and full rounds 0.32 and 0.65 us (53 bytes per ns of operands through the
+// L2).  Measured for 64 x 64: four one-step stages against two of two steps,
+// 128 x 4096 x 9600 27.9 and 31.0 us, 16 x 12000 x 9600 28 and 41, full rounds
+// 6 % slower; three stages and three workgroups per unit, 700 rows in 16
+// groups x 2048 x 4096 46 against 38.5 us.
+template <int BM, int BN, int KS, int NS>
 __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
   constexpr int FM = BM / 32, FN = BN / 32, ABLK = BM / 32, BBLK = BN / 32;
   constexpr int AB = BM * 128, BB = BN * 128, STAGE = KS * (AB + BB);
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+  constexpr int AHEAD = (NS - 2) * KS * (ABLK + BBLK);   // a wave's DMAs of the stages after the next one
+  // a tile's scales and biases, in NS + 1 slots (with one stage per tile, NS
+  // tiles are in flight when a finished one is stored): [BM row scales][BN channel
+  // scales][BN biases].  By DMA like the operands: the compiler's own loads
+  // in the loop would make it wait for every DMA behind them.
+  constexpr int SB_OFF = 4 * BM, BIAS_OFF = SB_OFF + 4 * BN, SCALES = BIAS_OFF + 256;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + (NS + 1) * SCALES];
   __shared__ GroupTable gt;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -456,53 +464,78 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
   const int64_t K = p.K, N = p.N;
   const int nst = (int)((K + 127) / 128), nsg = (nst + KS - 1) / KS;
   const int rem = (int)(K - 128 * (int64_t)(nst - 1));
-  const u32x4 rzero = rsrc4(p.A, 0);
+  constexpr uint32_t NOWHERE = 0x80000000u;    // past any resource: zeros, no memory read
   const int piece = (lane & 7) ^ kswz(lane >> 3);
   const uint32_t vo = (uint32_t)((lane >> 3) * K) + (uint32_t)(piece << 4);
-  const uint32_t vo_tail = 16 * piece < rem ? vo : 0x80000000u;
+  const uint32_t vo_tail = 16 * piece < rem ? vo : NOWHERE;
   const uint32_t lds0 = lds_addr(smem);
+  const uint32_t row8 = (uint32_t)(8 * K), arow = (uint32_t)(ABLK * w) * row8, brow = (uint32_t)(BBLK * w) * row8;
 
   struct Src {
-    u32x4 ra, rb;
-    int vrows;
+    int64_t row0, n0;
+    int g;
+    u32x4 ra, rb;                  // ra ends with the tile's rows: those past them read zeros
   };
   auto make_src = [&](int64_t i) {
     const StreamTile t = tile_at(i);
     Src s;
-    const int64_t abase = t.row0 * K, bbase = ((int64_t)t.g * N + t.n0) * K;
-    s.ra = rsrc4(p.A + abase, clamp_records(p.M * K - abase));
+    const int64_t bbase = ((int64_t)t.g * N + t.n0) * K;
+    s.row0 = t.row0;
+    s.n0 = t.n0;
+    s.g = t.g;
+    s.ra = rsrc4(p.A + t.row0 * K, clamp_records((t.lim - t.row0) * K));
     s.rb = rsrc4(p.B + bbase, clamp_records((int64_t)p.G * N * K - bbase));
-    const int64_t left = t.lim - t.row0;
-    s.vrows = (int)(left < BM ? left : BM);
     return s;
   };
   Src src = make_src(0);
   int64_t iss_i = 0;
-  int iss_sg = 0;
+  int iss_sg = 0, iss_sc = 0;
   // The next stage into slot sl; K steps past the tile's last and stages
-  // past the workgroup's last read an empty range.
+  // past the workgroup's last read nothing.  With a tile's first stage wave 0
+  // brings its row scales, wave 1 its channel scales, wave 2 its biases.
   auto issue = [&](int sl) {
     const bool real = iss_i < ntile;
+    if (real && iss_sg == 0) {
+      const uint32_t dst = lds0 + (uint32_t)(NS * STAGE + iss_sc * SCALES);
+      if (w == 0) {
+        const u32x4 r = rsrc4(p.sA + src.row0, clamp_records(4 * (p.M - src.row0)));
+        static_for<0, BM / 64>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          dma_asm_v<4, j * 256>(dst, r, (uint32_t)(lane * 4), j * 256u);
+        });
+      } else if (w == 1) {
+        const u32x4 r = rsrc4(p.sB + (int64_t)src.g * N + src.n0, clamp_records(4 * (N - src.n0)));
+        static_for<0, BN / 64>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          dma_asm_v<4, SB_OFF + j * 256>(dst, r, (uint32_t)(lane * 4), j * 256u);
+        });
+      } else if (w == 2) {
+        // without a bias an empty resource: the DMA writes zeros
+        const u32x4 r = p.bias ? rsrc4(p.bias + src.n0, clamp_records(2 * (N - src.n0))) : rsrc4(p.D, 0u);
+        dma_asm_v<4, BIAS_OFF>(dst, r, (uint32_t)(lane * 4), 0u);
+      }
+    }
     const uint32_t slot = lds0 + (uint32_t)sl * STAGE;
     static_for<0, KS>([&](auto sc) {
       constexpr int s = decltype(sc)::value;
       const int st = iss_sg * KS + s;
       const bool live = real && st < nst;
-      const uint32_t ka = slot + (uint32_t)s * AB, kb = slot + (uint32_t)(KS * AB + s * BB);
-      const uint32_t va = st == nst - 1 ? vo_tail : vo;
+      const uint32_t k0 = 128u * (uint32_t)st;
+      const uint32_t va = live ? (st == nst - 1 ? vo_tail : vo) + k0 : NOWHERE, vb = live ? vo + k0 : NOWHERE;
+      const uint32_t ka = slot + (uint32_t)(s * AB + ABLK * 1024 * w);
+      const uint32_t kb = slot + (uint32_t)(KS * AB + s * BB + BBLK * 1024 * w);
       static_for<0, ABLK>([&](auto jc) {
-        const int blk = ABLK * w + decltype(jc)::value;
-        const u32x4 ra = (live && blk * 8 < src.vrows) ? src.ra : rzero;
-        dma_asm_v<16>(ka + (uint32_t)blk * 1024u, ra, va, (uint32_t)(blk * 8 * K + 128 * (int64_t)st));
+        constexpr int j = decltype(jc)::value;
+        dma_asm_v<16, j * 1024>(ka, src.ra, va, arow + j * row8);
       });
-      const u32x4 rb = live ? src.rb : rzero;
       static_for<0, BBLK>([&](auto jc) {
-        const int blk = BBLK * w + decltype(jc)::value;
-        dma_asm_v<16>(kb + (uint32_t)blk * 1024u, rb, vo, (uint32_t)(blk * 8 * K + 128 * (int64_t)st));
+        constexpr int j = decltype(jc)::value;
+        dma_asm_v<16, j * 1024>(kb, src.rb, vb, brow + j * row8);
       });
     });
     if (++iss_sg == nsg) {
       iss_sg = 0;
+      iss_sc = iss_sc == NS ? 0 : iss_sc + 1;
       ++iss_i;
       if (iss_i < ntile) src = make_src(iss_i);
     }
@@ -517,57 +550,195 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
   const uint32_t p0 = (uint32_t)((q ^ f) << 4), p1 = (uint32_t)(((q + 4) ^ f) << 4);
   const uint32_t oa = (uint32_t)((wm * (BM / 2) + i16) * 128), ob = (uint32_t)((wn * (BN / 2) + i16) * 128);
 
-  issue(0);
-  wait_vmem_le<0>();
+  auto finish_tile = [&](auto ac, const StreamTile &t, uint32_t sc) {
+    constexpr int ACT = decltype(ac)::value;
+    v4f sb[FN], bias[FN];
+#pragma unroll
+    for (int b = 0; b < FN; ++b) {
+      const uint32_t o = (uint32_t)(wn * (BN / 2) + b * 16 + 4 * q);
+      const v4i s = *(const lds_v4i *)(uintptr_t)(sc + SB_OFF + 4 * o);
+      sb[b] = __builtin_bit_cast(v4f, s);
+      const v2i u = *(const lds_v2i *)(uintptr_t)(sc + BIAS_OFF + 2 * o);
+      bias[b] = unpack_bf16x4(u);
+    }
+    const int64_t r0 = t.row0 + wm * (BM / 2) + i16;
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      const float sa = __uint_as_float(*(const lds_u32_t *)(uintptr_t)(sc + (uint32_t)(4 * (wm * (BM / 2) + a * 16 + i16))));
+      if (r0 + a * 16 < t.lim) {
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+          int8_store4(p, ACT, r0 + a * 16, t.n0 + wn * (BN / 2) + b * 16 + 4 * q,
+                      int8_finish(acc[a][b], sa, sb[b], bias[b], ACT));
+      }
+    }
+  };
+
+  // Fragments of half h (64 of a step's 128 bytes of K) of the stage at stg.
+  // Two register sets: a half is read while the half before it runs on the
+  // matrix cores, across the barrier too.
+  v4i fa[2][FM], fb[2][FN];
+  auto read_half = [&](const uint8_t *stg, auto hc) {
+    constexpr int h = decltype(hc)::value, s = h >> 1, set = h & 1;
+    const uint32_t pc = set ? p1 : p0;
+    const uint8_t *la = stg + s * AB + oa + pc, *lb = stg + KS * AB + s * BB + ob + pc;
+#pragma unroll
+    for (int b = 0; b < FN; ++b) fb[set][b] = lds_read16(lb + b * 2048);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) fa[set][a] = lds_read16(la + a * 2048);
+  };
+  auto multiply = [&](auto sc) {
+    constexpr int set = decltype(sc)::value;
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(fb[set][b], fa[set][a], acc[a][b]);
+  };
+
+  // Stage v + NS goes into the slot of stage v once every wave has read v's
+  // last half.
+  static_for<0, NS>([&](auto sc) { issue(decltype(sc)::value); });
+  wait_vmem_le<AHEAD + KS * (ABLK + BBLK)>();
   __syncthreads();
+  read_half(smem, std::integral_constant<int, 0>{});
   int64_t ci = 0;
-  int csg = 0;
+  int csg = 0, slot = 0, csc = 0;
   const int64_t V = ntile * nsg;
   for (int64_t v = 0; v < V; ++v) {
-    issue((int)((v + 1) & 1));
-    const uint8_t *stg = smem + (v & 1) * STAGE;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const uint8_t *la = stg + s * AB + oa, *lb = stg + KS * AB + s * BB + ob;
-      v4i b0[FN], b1[FN];
-#pragma unroll
-      for (int b = 0; b < FN; ++b) {
-        b0[b] = lds_read16(lb + p0 + b * 2048);
-        b1[b] = lds_read16(lb + p1 + b * 2048);
-      }
-#pragma unroll
-      for (int a = 0; a < FM; ++a) {
-        const v4i a0 = lds_read16(la + p0 + a * 2048), a1 = lds_read16(la + p1 + a * 2048);
-#pragma unroll
-        for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(b0[b], a0, acc[a][b]);
-#pragma unroll
-        for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(b1[b], a1, acc[a][b]);
-      }
-    }
-    if (++csg == nsg) {
-      const StreamTile t = tile_at(ci);
-      v4f sb[FN], bias[FN];
-#pragma unroll
-      for (int b = 0; b < FN; ++b) int8_columns(p, t.g, t.n0 + wn * (BN / 2) + b * 16 + 4 * q, sb[b], bias[b]);
-#pragma unroll
-      for (int a = 0; a < FM; ++a) {
-        const int64_t row = t.row0 + wm * (BM / 2) + a * 16 + i16;
-        const bool in = row < t.lim;
-        const float sa = in ? p.sA[row] : 0.0f;
-#pragma unroll
-        for (int b = 0; b < FN; ++b) {
-          if (in)
-            int8_store4(p, p.act, row, t.n0 + wn * (BN / 2) + b * 16 + 4 * q, int8_finish(acc[a][b], sa, sb[b], bias[b], p.act));
-          acc[a][b] = (v4i){0, 0, 0, 0};
-        }
-      }
-      csg = 0;
-      ++ci;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmem_le<0>();   // stage v + 1
+    static_for<1, 2 * KS>([&](auto hc) {
+      constexpr int h = decltype(hc)::value;
+      read_half(smem + slot * STAGE, std::integral_constant<int, h>{});
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(std::integral_constant<int, (h - 1) & 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // stage v + 1 has landed (stores of a tile are newer: more is waited for)
+    // and this wave's reads of stage v are done
+    __builtin_amdgcn_s_waitcnt(0x0070 | (AHEAD & 15) | ((AHEAD >> 4) << 14));
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
+    issue(slot);
+    slot = slot + 1 == NS ? 0 : slot + 1;
+    read_half(smem + slot * STAGE, std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(std::integral_constant<int, 1>{});
+    if (++csg == nsg) {
+      const StreamTile t = tile_at(ci);
+      const uint32_t sc = lds0 + (uint32_t)(NS * STAGE + csc * SCALES);
+      if (p.act == ACT_NONE) finish_tile(std::integral_constant<int, ACT_NONE>{}, t, sc);
+      else if (p.act == ACT_SWIGLU) finish_tile(std::integral_constant<int, ACT_SWIGLU>{}, t, sc);
+      else if (p.act == ACT_GELU_TANH) finish_tile(std::integral_constant<int, ACT_GELU_TANH>{}, t, sc);
+      else if (p.act == ACT_SILU) finish_tile(std::integral_constant<int, ACT_SILU>{}, t, sc);
+      else finish_tile(std::integral_constant<int, ACT_RELU>{}, t, sc);
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b) acc[a][b] = (v4i){0, 0, 0, 0};
+      csg = 0;
+      csc = csc == NS ? 0 : csc + 1;
+      ++ci;
+    }
+    // accumulators in VGPRs: with one workgroup per compute unit the compiler
+    // moved them to AGPRs and back in every step
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b) asm volatile("" : "+v"(acc[a][b]));
+  }
+  wait_vmem_le<0>();   // no DMA into the LDS of an ended workgroup
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: BM = 16 FM rows x BN = 16 FN columns per workgroup of W waves that
+// split K between them, step st of 128 bytes to wave st % W.  Operands go from
+// memory straight to registers in the matrix cores' layout (nothing is shared
+// between waves but the final sum, so LDS staging and its barriers would only
+// add latency), U steps ahead; the waves' integer partial sums meet in LDS.
+template <int FM, int FN, int W, int U>
+__global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args p) {
+  constexpr int BM = 16 * FM, BN = 16 * FN;
+  __shared__ v4i part[W][FM * FN][64];
+  __shared__ GroupTable gt;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, q = lane >> 4;
+  if (w == 0) int8_group_table<BM>(p, gt, lane);
+  __syncthreads();
+  // eight contiguous bands of tiles, one per XCD: the row tiles of one set of
+  // columns read the same weights
+  const int64_t T = (int64_t)uni32(gt.mtile[p.G]) * p.tiles_n;
+  const int x = (int)(blockIdx.x & 7), r = (int)(blockIdx.x >> 3);
+  const int64_t lo = T & 7, band = (T >> 3) + (x < lo ? 1 : 0);
+  if (r >= band) return;
+  GroupedArgs ga = {};
+  ga.G = p.G;
+  ga.tiles_n = p.tiles_n;
+  const StreamTile t = stream_tile<BM, BN>(ga, gt, x * (T >> 3) + (x < lo ? x : lo) + r);
+
+  const int64_t K = p.K, N = p.N;
+  const int nst = (int)((K + 127) / 128);
+  const int64_t abase = t.row0 * K, bbase = ((int64_t)t.g * N + t.n0) * K;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A + abase, clamp_records(p.M * K - abase));
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.B + bbase, clamp_records((int64_t)p.G * N * K - bbase));
+  constexpr uint32_t NOWHERE = 0x80000000u;    // past any resource: zeros, no memory read
+  const uint32_t lane_off = (uint32_t)(i16 * K + 16 * q);
+  uint32_t rows_a[FM];
+#pragma unroll
+  for (int a = 0; a < FM; ++a) rows_a[a] = t.row0 + 16 * a + i16 < t.lim ? lane_off + (uint32_t)(16 * a * K) : NOWHERE;
+
+  v4i fa[U][FM][2], fb[U][FN][2];
+  auto load = [&](int u, int st) {
+    const uint32_t k0 = (uint32_t)st * 128u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = (int64_t)st * 128 + 64 * h + 16 * q < K;
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+        fb[u][b][h] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(in ? lane_off + (uint32_t)(16 * b * K) + k0 + 64u * h : NOWHERE), 0, 0));
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+        fa[u][a][h] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                     ra, (int)(in && rows_a[a] != NOWHERE ? rows_a[a] + k0 + 64u * h : NOWHERE), 0, 0));
+    }
+  };
+  v4i acc[FM][FN];
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) acc[a][b] = (v4i){0, 0, 0, 0};
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, w + u * W);
+  for (int st = w; st < nst; st += U * W) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+          for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(fb[u][b][h], fa[u][a][h], acc[a][b]);
+      if (st + U * W < nst) load(u, st + (u + U) * W);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) part[w][a * FN + b][lane] = acc[a][b];
+  __syncthreads();
+#pragma unroll
+  for (int f = w; f < FM * FN; f += W) {
+    const int a = f / FN, b = f % FN;
+    v4i sum = part[0][f][lane];
+#pragma unroll
+    for (int k = 1; k < W; ++k) sum += part[k][f][lane];
+    const int64_t row = t.row0 + 16 * a + i16, col = t.n0 + 16 * b + 4 * q;
+    if (row < t.lim) {
+      v4f sb, bias;
+      int8_columns(p, t.g, t.n0, 16 * b + 4 * q, sb, bias);
+      int8_store4(p, p.act, row, col, int8_finish(sum, p.sA[row], sb, bias, p.act));
+    }
   }
 }
 

@@ -18,16 +18,52 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   return MXG_OK;
 }
 
-// Kernel of a product of G groups with at most M rows in all, from upper
-// bounds of the tile counts (MXG_GROUPED_*).
+// The kernels: streaming through registers in 16 x 16 or 32 x 32 tiles,
+// through LDS in 64 x 64 or 128 x 128 tiles, 256 x 256 tiles.
+enum Kernel { ROWS16, ROWS32, STREAM64, STREAM128, TILED };
+
+// Estimated microseconds of each kernel, from static shapes alone (m_sizes
+// stays on the device: each group is taken to end inside a row tile).  The
+// constants are fitted to 122 dense and grouped calls of 1 .. 16384 rows, all
+// kernels timed on each; there the choice is the fastest kernel or within 14 %
+// of it, 0.9 % on average.  Both sides where the choice turns: 3 x 3829 x
+// 3984 takes 5.9 us in ROWS16 and 14.4 in STREAM64, 65 x 12000 x 4096 55 and
+// 17; 200 x 2000 x 400 5.3 in ROWS32 and 5.9 in STREAM64, 777 x 5002 x 4112
+// 84 and 49, 38 in STREAM128; 2049 x 8000 x 2064 68 in STREAM128 and 58 in
+// TILED, 6449 x 1003 x 1040 22 and 28.
+Kernel choose(int G, int64_t M, int64_t N, int64_t K) {
+  if (G < 1 || M <= 0 || N <= 0 || K <= 0) return STREAM64;
+  const double cus = cu_count(), nst = (double)cdiv(K, 128), live = (double)std::min<int64_t>(G, M);
+  auto tiles = [&](int b) { return (G == 1 ? (double)cdiv(M, b) : (double)M / b + 0.5 * live) * (double)cdiv(N, b); };
+  // memory: weights, activations and output once, 6.9 TB/s
+  const double mem = (live * (double)N * (double)K + (double)M * (double)K + 2.0 * (double)M * (double)N) / 6.9e6;
+  double t[5];
+  // ROWS: a compute unit's 36 (30) bytes per ns of operands, tiles of full rows
+  auto rows = [&](int b, double t0, double rate, double per_tile) {
+    const double n = tiles(b), bytes = (std::min((double)b, (double)M / live) + b) * (double)K;
+    return t0 + std::max(std::max(1.0, n / cus) * bytes / rate, mem) + per_tile * n / cus;
+  };
+  t[ROWS16] = rows(16, 3.2, 35.9e3, 0.27);
+  t[ROWS32] = rows(32, 3.6, 29.7e3, 0.52);
+  // STREAM: two workgroups per compute unit, a K step's time in a round of tiles
+  auto stream = [&](int b, double t0, double alone, double shared, double per_tile) {
+    const double n = tiles(b), step = n <= cus ? alone : shared * std::ceil(n / (2 * cus));
+    return t0 + std::max(nst * step, mem) + per_tile * n / (2 * cus);
+  };
+  t[STREAM64] = stream(64, 3.5, 0.36, 0.65, 0.6);
+  t[STREAM128] = stream(128, 4.3, 0.80, 1.31, 2.9);
+  const double nt = tiles(DBM);
+  t[TILED] = 3.6 + std::ceil(nt / cus) * (nst * (nt <= cus ? 1.28 : 1.71) + 6.4);
+  return (Kernel)(std::min_element(t, t + 5) - t);
+}
+
 int int8_variant(int G, int64_t M, int64_t N, int64_t K) {
-  if (G < 1 || M <= 0 || N <= 0 || K <= 0) return MXG_GROUPED_STREAM64;
-  const double cus = cu_count(), nst = (double)cdiv(K, 128);
-  const double t64 = 0.8 * (double)(cdiv(M, 64) + G - 1) * (double)cdiv(N, 64) * nst / (2 * cus);
-  const double t128 = std::max(1.6 * (double)(cdiv(M, 128) + G - 1) * (double)cdiv(N, 128) * nst / (2 * cus), 1.1 * nst);
-  const double td = std::ceil((double)(cdiv(M, DBM) + G - 1) * (double)cdiv(N, DBN) / cus) * (1.4 * nst + 10.0);
-  if (t64 <= t128 && t64 <= td) return MXG_GROUPED_STREAM64;
-  return t128 <= td ? MXG_GROUPED_STREAM128 : MXG_GROUPED_TILED;
+  switch (choose(G, M, N, K)) {
+    case STREAM64: return MXG_GROUPED_STREAM64;
+    case STREAM128: return MXG_GROUPED_STREAM128;
+    case TILED: return MXG_GROUPED_TILED;
+    default: return MXG_GROUPED_ROWS;
+  }
 }
 
 int launch(Int8Args &a, hipStream_t stream) {
@@ -38,27 +74,42 @@ int launch(Int8Args &a, hipStream_t stream) {
     hipLaunchKernelGGL(int8_fill_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
     return launch_status();
   }
-  const int v = int8_variant(a.G, a.M, a.N, a.K);
-  const bool tiled = v == MXG_GROUPED_TILED;
-  const int BT = tiled ? DBM : (v == MXG_GROUPED_STREAM64 ? 64 : 128);
+  const Kernel k = choose(a.G, a.M, a.N, a.K);
+  const int BT = k == ROWS16 ? 16 : k == ROWS32 ? 32 : k == STREAM64 ? 64 : k == STREAM128 ? 128 : DBM;
   a.tiles_n = (int)cdiv(a.N, BT);
   const int64_t tiles = (cdiv(a.M, BT) + a.G - 1) * a.tiles_n;
-  if (tiles > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
-  if (tiled) {
-    const unsigned grid = (unsigned)std::min<int64_t>(tiles, cu_count());
-    void (*fn)(Int8Args) = a.act == ACT_SWIGLU      ? int8_tiled_kernel<ACT_SWIGLU>
-                           : a.act == ACT_RELU      ? int8_tiled_kernel<ACT_RELU>
-                           : a.act == ACT_GELU_TANH ? int8_tiled_kernel<ACT_GELU_TANH>
-                           : a.act == ACT_SILU      ? int8_tiled_kernel<ACT_SILU>
-                                                    : int8_tiled_kernel<ACT_NONE>;
-    hipLaunchKernelGGL(fn, dim3(grid), dim3(DNW8 * 64), 0, stream, a);
-  } else {
-    const unsigned grid = (unsigned)std::min<int64_t>(tiles, 2ll * cu_count());
-    if (BT == 64)
-      hipLaunchKernelGGL((int8_stream_kernel<64, 64, 2>), dim3(grid), dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((int8_stream_kernel<128, 128, 1>), dim3(grid), dim3(256), 0, stream, a);
+  if (tiles > 0x7FFFFFF0) return MXG_ERR_UNSUPPORTED;
+  void (*fn)(Int8Args);
+  int64_t grid = 0;
+  int threads = 256;
+  switch (k) {
+    case ROWS16:
+      fn = int8_rows_kernel<1, 1, 4, 4>;
+      grid = (tiles + 7) / 8 * 8;          // eight bands (XCDs) of equal length
+      break;
+    case ROWS32:
+      fn = int8_rows_kernel<2, 2, 8, 2>;
+      grid = (tiles + 7) / 8 * 8;
+      threads = 512;
+      break;
+    case STREAM64:
+      fn = int8_stream_kernel<64, 64, 1, 4>;
+      grid = std::min<int64_t>(tiles, 2ll * cu_count());
+      break;
+    case STREAM128:
+      fn = int8_stream_kernel<128, 128, 1, 2>;
+      grid = std::min<int64_t>(tiles, 2ll * cu_count());
+      break;
+    default:
+      fn = a.act == ACT_SWIGLU      ? int8_tiled_kernel<ACT_SWIGLU>
+           : a.act == ACT_RELU      ? int8_tiled_kernel<ACT_RELU>
+           : a.act == ACT_GELU_TANH ? int8_tiled_kernel<ACT_GELU_TANH>
+           : a.act == ACT_SILU      ? int8_tiled_kernel<ACT_SILU>
+                                    : int8_tiled_kernel<ACT_NONE>;
+      grid = std::min<int64_t>(tiles, cu_count());
+      threads = DNW8 * 64;
   }
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, a);
   return launch_status();
 }
 
