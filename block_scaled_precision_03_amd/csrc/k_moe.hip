@@ -139,7 +139,7 @@ extern "C" int moe_route(int dtype, const void *logits, const float *bias, int32
   const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(256, cdiv(per_block * s.lpt, 64) * 64));
   route_fn fn = dtype == MXG_BF16 ? pick_route<uint16_t>(s, maps, one) : pick_route<float>(s, maps, one);
   hipLaunchKernelGGL(fn, dim3((unsigned)a.nblk), dim3((unsigned)threads), 0, stream, a);
-  if (maps && !one) hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)a.nblk), dim3(256), 0, stream, a);
+  if (maps && !one) hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)a.nblk), dim3(a.nblk > 32 ? 1024 : 256), 0, stream, a);
   return launch_status();
 }
 

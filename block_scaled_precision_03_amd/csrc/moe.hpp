@@ -44,53 +44,226 @@ struct RoutePlace {
   int32_t used;
 };
 
-// One token's choice by LPT lanes (its lanes hold `per` <= VPT consecutive
-// experts each; an expert group owns lpg consecutive lanes, so a group's
-// statistics need no more than shuffles among them), `sub` the lane's index
-// among them.  Choice values in 64 bits: scores that differ in FP32's last
-// bits decide between experts.  Returns the id of rank `sub` (-1: none) in
-// lanes sub < topk, and its weight.
-template <class IN, int LPT, int VPT>
-__device__ inline int route_token(const RouteArgs &p, const IN *row, bool live, int sub, float &weight) {
-  const int n = p.E / p.n_group;
-  const int gi = sub / p.lpg, part = sub % p.lpg;
-  const int e0 = gi * n + part * p.per;
-  const int cnt = (live && gi < p.n_group) ? max(0, min(p.per, n - part * p.per)) : 0;
-  const double NONE = -__builtin_inf();
-  float l[VPT];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) l[j] = j < cnt ? load_elem(row + e0 + j) : -__builtin_inff();
-  // finite stand-in of an available logit; NaN and -inf are not available
-  auto avail = [](float x) { return x > -__builtin_inff(); };
-  auto fin = [](float x) { return (double)fminf(x, 3.402823466e38f); };
+// x of the lane that the DPP control names (within 16 lanes).
+template <int CTRL>
+__device__ inline int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ inline float dpp(float x) {
+  return __int_as_float(dpp<CTRL>(__float_as_int(x)));
+}
+template <int CTRL>
+__device__ inline double dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint64_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp<CTRL>((int)(u >> 32));
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+// x of both members of the lane's pair of 16-lane rows (HALF: of wave halves).
+template <bool HALF>
+__device__ inline void both(int x, int &y0, int &y1) {
+  if constexpr (HALF) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    y0 = r[0], y1 = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    y0 = r[0], y1 = r[1];
+  }
+}
+template <bool HALF>
+__device__ inline void both(double x, double &y0, double &y1) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  int l0, l1, h0, h1;
+  both<HALF>((int)(uint32_t)u, l0, l1);
+  both<HALF>((int)(u >> 32), h0, h1);
+  y0 = __builtin_bit_cast(double, (uint64_t)(uint32_t)h0 << 32 | (uint32_t)l0);
+  y1 = __builtin_bit_cast(double, (uint64_t)(uint32_t)h1 << 32 | (uint32_t)l1);
+}
+// op over each run of LPT (16 or 64) lanes, in all of them: lane exchanges
+// in registers (neighbours, pairs, mirrored eights and sixteens, rows,
+// halves), with no trip through LDS.
+template <bool HALF>
+__device__ inline void both(float x, float &y0, float &y1) {
+  int a, b;
+  both<HALF>(__float_as_int(x), a, b);
+  y0 = __int_as_float(a), y1 = __int_as_float(b);
+}
+template <int LPT, class T, class Op>
+__device__ inline T lanes_reduce(T x, Op op) {
+  x = op(x, dpp<0xB1>(x));               // quad_perm 1 0 3 2
+  x = op(x, dpp<0x4E>(x));               // quad_perm 2 3 0 1
+  x = op(x, dpp<0x141>(x));              // row_half_mirror
+  x = op(x, dpp<0x140>(x));              // row_mirror
+  if constexpr (LPT == 64) {
+    T a, b;
+    both<false>(x, a, b);
+    x = op(a, b);
+    both<true>(x, a, b);
+    x = op(a, b);
+  }
+  return x;
+}
+struct OpMax {
+  __device__ double operator()(double a, double b) const { return fmax(a, b); }
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct OpAdd { __device__ double operator()(double a, double b) const { return a + b; } };
+struct OpMin {
+  __device__ int operator()(int a, int b) const { return min(a, b); }
+  __device__ float operator()(float a, float b) const { return fminf(a, b); }
+};
 
-  double m = NONE, sum = 0.0;
-  if (p.score == MOE_SOFTMAX) {
+// e^-t for t >= 0 in 64 bits, within about an ulp: -t = n ln 2 + r, |r| <=
+// ln 2 / 2, ln 2 in two parts (the first of 32 bits: n times it is exact),
+// the exponential series of r to r^13 (the rest is below 2^-57).
+__device__ inline double exp_neg(double t) {
+  t = fmin(t, 750.0);                    // e^-750 < 2^-1075
+  const double n = rint(t * -1.4426950408889634);
+  const double r = fma(n, -1.90821492927058770002e-10, fma(n, -6.93147180369123816490e-01, -t));
+  double q = 1.0 / 6227020800.0;
+  q = fma(q, r, 1.0 / 479001600.0);
+  q = fma(q, r, 1.0 / 39916800.0);
+  q = fma(q, r, 1.0 / 3628800.0);
+  q = fma(q, r, 1.0 / 362880.0);
+  q = fma(q, r, 1.0 / 40320.0);
+  q = fma(q, r, 1.0 / 5040.0);
+  q = fma(q, r, 1.0 / 720.0);
+  q = fma(q, r, 1.0 / 120.0);
+  q = fma(q, r, 1.0 / 24.0);
+  q = fma(q, r, 1.0 / 6.0);
+  q = fma(q, r, 0.5);
+  q = fma(q, r, 1.0);
+  q = fma(q, r, 1.0);
+  return __builtin_ldexp(q, (int)n);
+}
+
+// 1 / d for d in [1, 2^1000] by two Newton steps from the hardware's estimate
+// (exact for d = 1).
+__device__ inline double recip(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = fma(fma(-d, r, 1.0), r, r);
+  return fma(fma(-d, r, 1.0), r, r);
+}
+
+// 1 / (1 + e^-x); 0 where e^-x is past 64 bits.
+__device__ inline double logistic(double x) {
+  const double t = fabs(x), e = exp_neg(t), r = recip(1.0 + e);
+  return x >= 0.0 ? r : (t > 709.78 ? 0.0 : e * r);
+}
+
+// The lane's `cnt` <= VPT consecutive logits, -inf past them: four at a time
+// (at any alignment) where all four are there.
+template <class IN, int VPT>
+__device__ inline void load_logits(const IN *p, int cnt, float (&l)[VPT]) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (avail(l[j])) m = fmax(m, fin(l[j]));
+  for (int j = 0; j < VPT; j += 4) {
+    if (j + 4 <= cnt) {
+      IN u[4];
+      __builtin_memcpy(u, p + j, sizeof(u));
 #pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) m = fmax(m, __shfl_xor(m, d, 64));
-    if (!p.renorm || p.bias || (p.n_group > 1 && p.group_score == MOE_GROUP_TOP2)) {
+      for (int k = 0; k < 4; ++k) l[j + k] = load_elem(u + k);
+    } else {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (avail(l[j])) sum += exp(fin(l[j]) - m);
-#pragma unroll
-      for (int d = 1; d < LPT; d <<= 1) sum += __shfl_xor(sum, d, 64);
+      for (int k = 0; k < 4; ++k) l[j + k] = j + k < cnt ? load_elem(p + j + k) : -__builtin_inff();
     }
   }
-  auto score = [&](double x) { return p.score == MOE_SOFTMAX ? exp(x - m) / sum : 1.0 / (1.0 + exp(-x)); };
+}
 
+// A token's LPT lanes hold `per` <= VPT consecutive experts each; an expert
+// group owns lpg consecutive lanes, so a group's statistics need no more than
+// shuffles among them.
+struct LaneSpan {
+  int gi, e0, cnt;                       // group, first expert, experts of this lane
+};
+__device__ inline LaneSpan lane_span(const RouteArgs &p, bool live, int sub) {
+  const int n = p.E / p.n_group;
+  LaneSpan s;
+  s.gi = sub / p.lpg;
+  const int part = sub % p.lpg;
+  s.e0 = s.gi * n + part * p.per;
+  s.cnt = (live && s.gi < p.n_group) ? max(0, min(p.per, n - part * p.per)) : 0;
+  return s;
+}
+
+// An available logit (not -inf, not NaN) and its finite stand-in.
+__device__ inline bool avail(float x) { return x > -__builtin_inff(); }
+__device__ inline float fin(float x) { return fminf(x, 3.402823466e38f); }
+
+// The largest available logit and 1 / (sum of e^(l - m)).
+template <int LPT, int VPT>
+__device__ inline void softmax_stats(const float (&l)[VPT], double &m, double &inv) {
+  float mm = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) mm = fmaxf(mm, avail(l[j]) ? fin(l[j]) : -__builtin_inff());
+  m = (double)lanes_reduce<LPT>(mm, OpMax());
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) sum += avail(l[j]) ? exp_neg(m - (double)fin(l[j])) : 0.0;
+  inv = recip(fmax(lanes_reduce<LPT>(sum, OpAdd()), 1.0));
+}
+
+// The largest two of the lane's group, from the lane's own.
+template <class T>
+__device__ inline void group_best(const RouteArgs &p, T &g1, T &g2) {
+  for (int d = 1; d < p.lpg; d <<= 1) {
+    const T o1 = __shfl_xor(g1, d, 64), o2 = __shfl_xor(g2, d, 64);
+    g2 = fmax(fmin(g1, o1), fmax(g2, o2));
+    g1 = fmax(g1, o1);
+  }
+}
+
+// How many groups come before the lane's.
+template <int LPT, class T>
+__device__ inline int group_rank(const RouteArgs &p, T gs, int gi) {
+  int rank = 0;
+  for (int g = 0; g < p.n_group; ++g) {
+    const T o = __shfl(gs, g * p.lpg, LPT);
+    rank += (o > gs || (o == gs && g < gi)) ? 1 : 0;
+  }
+  return rank;
+}
+
+// One rank of the choice: the largest value over the lanes, then the lowest
+// expert that holds it, which becomes NaN (no maximum takes it); -1: none.
+template <int LPT, int VPT, class T>
+__device__ inline int take_best(T (&v)[VPT], int e0, int cnt, T &best) {
+  T bv = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) bv = fmax(bv, v[j]);
+  bv = lanes_reduce<LPT>(bv, OpMax());
+  int be = 0x7FFFFFFF;
+#pragma unroll
+  for (int j = VPT - 1; j >= 0; --j) be = v[j] == bv ? e0 + j : be;
+  be = lanes_reduce<LPT>(be, OpMin());
+  best = bv;
+  const int chosen = bv > -__builtin_inff() ? be : -1, at = chosen - e0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (at == j && j < cnt) v[j] = __builtin_nanf("");
+  return chosen;
+}
+
+// The choice with every value in 64 bits.  Lane `sub` < topk returns the id
+// of rank `sub`.
+template <class IN, int LPT, int VPT>
+__device__ inline int choose64(const RouteArgs &p, const IN *row, const LaneSpan &sp, int sub) {
+  const double NONE = -__builtin_inf();
+  float l[VPT];
+  load_logits<IN, VPT>(row + sp.e0, sp.cnt, l);
+  const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
+  double m = 0.0, inv = 0.0;
+  if (p.score == MOE_SOFTMAX) softmax_stats<LPT>(l, m, inv);
   double v[VPT];
   double g1 = NONE, g2 = NONE;           // the lane's two best of its group
+  float b[VPT];
+  if (p.bias) load_logits<float, VPT>(p.bias + sp.e0, sp.cnt, b);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     v[j] = NONE;
     if (avail(l[j])) {
-      double s = 0.0;
-      const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
-      if (p.bias || top2) s = score(fin(l[j]));
-      if (p.bias) s += (double)p.bias[e0 + j];
+      const double x = (double)fin(l[j]);
+      double s = p.score == MOE_SOFTMAX ? exp_neg(m - x) * inv : logistic(x);
+      if (p.bias) s += (double)b[j];
       v[j] = p.bias ? s : (double)l[j];
       const double gv = top2 ? s : v[j];
       g2 = fmax(g2, fmin(g1, gv));
@@ -98,69 +271,140 @@ __device__ inline int route_token(const RouteArgs &p, const IN *row, bool live, 
     }
   }
   if (p.n_group > 1) {
-    for (int d = 1; d < p.lpg; d <<= 1) {
-      const double o1 = __shfl_xor(g1, d, 64), o2 = __shfl_xor(g2, d, 64);
-      g2 = fmax(fmin(g1, o1), fmax(g2, o2));
-      g1 = fmax(g1, o1);
-    }
-    double gs = g1;
-    if (p.group_score == MOE_GROUP_TOP2 && g2 > NONE) gs += g2;
-    int rank = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const double o = __shfl(gs, g * p.lpg, LPT);
-      rank += (o > gs || (o == gs && g < gi)) ? 1 : 0;
-    }
-    if (rank >= p.topk_group) {
+    group_best(p, g1, g2);
+    if (group_rank<LPT>(p, top2 && g2 > NONE ? g1 + g2 : g1, sp.gi) >= p.topk_group) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) v[j] = NONE;
     }
   }
-
   int id = -1;
   for (int r = 0; r < p.topk; ++r) {
-    double bv = NONE;
-    int be = 0x7FFFFFFF;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (v[j] > bv) {
-        bv = v[j];
-        be = e0 + j;
-      }
-#pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) {
-      const double ov = __shfl_xor(bv, d, 64);
-      const int oe = __shfl_xor(be, d, 64);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    const int chosen = bv > NONE ? be : -1;
-    if (sub == r) id = chosen;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (e0 + j == chosen && j < cnt) v[j] = NONE;
+    double best;
+    const int c = take_best<LPT>(v, sp.e0, sp.cnt, best);
+    if (sub == r) id = c;
   }
+  return id;
+}
+
+// The choice from values in 32 bits, where they can decide it.  Without a
+// bias they are the logits themselves.  A sigmoid's score plus bias is within
+// 4e-7 + 6e-8 |value| of the exact sum (the exponential and the reciprocal
+// one unit in the last place each, one rounding for the sum), so values
+// further apart than `apart` are in their exact order: the best topk + 1
+// experts by 32 bits hold the topk best wherever the topk-th is so far from
+// the first one left, and 64-bit values of these candidates alone, one per
+// lane, give the choice and its order.  Groups are decided by 32 bits where
+// the last kept and the first dropped are far enough apart.  `open` is set
+// where this does not decide (about one token in 5000), for choose64.
+// 16384 tokens of 256 experts in 8 groups, 8 chosen by sigmoid and bias: 35 us
+// with all values in 64 bits.
+template <class IN, int LPT, int VPT>
+__device__ inline int choose32(const RouteArgs &p, const IN *row, const LaneSpan &sp, int sub, bool &open) {
+  const float NONE = -__builtin_inff();
+  float v[VPT];
+  load_logits<IN, VPT>(row + sp.e0, sp.cnt, v);
+  const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
+  auto apart = [](float hi, float lo) { return lo == -__builtin_inff() || hi - lo > 1.6e-6f + 2.5e-7f * (fabsf(hi) + fabsf(lo)); };
+  float g1 = NONE, g2 = NONE;
+  if (p.bias || top2) {
+    float b[VPT];
+    if (p.bias) load_logits<float, VPT>(p.bias + sp.e0, sp.cnt, b);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool ok = avail(v[j]);
+      const float s = logistic_f32(v[j]) + (p.bias ? b[j] : 0.0f);
+      v[j] = ok ? (p.bias ? s : v[j]) : NONE;
+      const float gv = ok ? (top2 ? s : v[j]) : NONE;
+      g2 = fmaxf(g2, fminf(g1, gv));
+      g1 = fmaxf(g1, gv);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      v[j] = avail(v[j]) ? v[j] : NONE;
+      g1 = fmaxf(g1, v[j]);
+    }
+  }
+  open = false;
+  if (p.n_group > 1) {
+    group_best(p, g1, g2);
+    const float gs = top2 && g2 > NONE ? g1 + g2 : g1;
+    const bool out = group_rank<LPT>(p, gs, sp.gi) >= p.topk_group;
+    if (p.bias || top2) {
+      const float kept = lanes_reduce<LPT>(out ? -NONE : gs, OpMin());
+      const float left = lanes_reduce<LPT>(out ? gs : NONE, OpMax());
+      open = !apart(kept, left);
+    }
+    if (out) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) v[j] = NONE;
+    }
+  }
+  int id = -1;
+  float last = NONE, next;
+  for (int r = 0; r < p.topk; ++r) {
+    const int c = take_best<LPT>(v, sp.e0, sp.cnt, last);
+    if (sub == r) id = c;
+  }
+  if (!p.bias) return id;
+  int cand = p.topk;
+  if (cand < LPT) {
+    const int c = take_best<LPT>(v, sp.e0, sp.cnt, next);
+    if (sub == cand) id = c;
+    ++cand;
+  }
+  float rest = NONE;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) rest = fmaxf(rest, v[j]);
+  open |= !apart(last, lanes_reduce<LPT>(rest, OpMax()));
+  // order by the 64-bit values; lanes past the last chosen stay where they are
+  double x = -__builtin_inf();
+  if (id >= 0) x = logistic((double)fin(load_elem(row + id))) + (double)p.bias[id];
+  int rank = 0;
+  for (int r = 0; r < cand; ++r) {
+    const double o = __shfl(x, r, LPT);
+    const int oid = __shfl(id, r, LPT);
+    rank += (o > x || (o == x && oid < id)) ? 1 : 0;
+  }
+  if (id < 0) rank = sub;
+  const int base = (int)(threadIdx.x & 63) - sub;
+  id = __builtin_amdgcn_ds_permute((base + rank) * 4, id);
+  return sub < p.topk ? id : -1;
+}
+
+// One token's choice and weights by LPT lanes: the id of rank `sub` (-1:
+// none) in lanes sub < topk, and its weight.  Scores that differ in FP32's
+// last bits decide between experts.
+template <class IN, int LPT, int VPT>
+__device__ inline int route_token(const RouteArgs &p, const IN *row, bool live, int sub, float &weight) {
+  const LaneSpan sp = lane_span(p, live, sub);
+  const bool sm = p.score == MOE_SOFTMAX;
+  bool open = true;
+  int id = -1;
+  if (!(sm && (p.bias || (p.n_group > 1 && p.group_score == MOE_GROUP_TOP2))))
+    id = choose32<IN, LPT, VPT>(p, row, sp, sub, open);
+  if (__any(open)) id = choose64<IN, LPT, VPT>(p, row, sp, sub);
 
   // weights, one rank per lane
   const bool has = id >= 0;
-  const double x = has ? fin(load_elem(row + id)) : 0.0;
+  const double x = has ? (double)fin(load_elem(row + id)) : 0.0;
   double w;
   if (p.renorm) {
     // shares of the chosen: a common factor e^-top keeps them in range
-    const bool sm = p.score == MOE_SOFTMAX;
-    double top = has ? (sm ? x : fmin(x, 0.0)) : NONE;
-    const double mine = top;
-#pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) top = fmax(top, __shfl_xor(top, d, 64));
+    const double mine = has ? (sm ? x : fmin(x, 0.0)) : -__builtin_inf();
+    const double top = lanes_reduce<LPT>(mine, OpMax());
     w = 0.0;
-    if (has) w = exp(mine - top) / (sm ? 1.0 : 1.0 + exp(-fabs(x)));
-    double tot = w;
-#pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) tot += __shfl_xor(tot, d, 64);
+    if (has) w = exp_neg(top - mine) * (sm ? 1.0 : recip(1.0 + exp_neg(fabs(x))));
+    const double tot = lanes_reduce<LPT>(w, OpAdd());
     w = has ? w / tot : 0.0;
+  } else if (sm) {
+    float l[VPT];
+    load_logits<IN, VPT>(row + sp.e0, sp.cnt, l);
+    double m, inv;
+    softmax_stats<LPT>(l, m, inv);
+    w = has ? exp_neg(m - x) * inv : 0.0;
   } else {
-    w = has ? score(x) : 0.0;
+    w = has ? logistic(x) : 0.0;
   }
   weight = (float)(w * (double)p.scale);
   return id;
@@ -290,17 +534,26 @@ __global__ void route_kernel(RouteArgs p) {
 // The second kernel of a call of more than 64 tokens: every block sums the
 // counts of all blocks (its own first rows and the experts' totals), then
 // places its tokens.
-__global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p) {
+// Up to 16 waves per block: with 256 threads a block of 16384 tokens' call
+// read the 128 KB of counts in 32 dependent rounds, 9.6 us.
+__global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
   __shared__ int32_t ids[ROUTE_TG * MOE_MAX_TOPK];
   __shared__ RoutePlace pl;
   const int tid = threadIdx.x;
-  for (int e = tid; e < MOE_MAX_E; e += 256) pl.total[e] = pl.base[e] = 0;
+  const int nthr = (int)blockDim.x;
+  for (int e = tid; e < MOE_MAX_E; e += nthr) pl.total[e] = pl.base[e] = 0;
   __syncthreads();
-  const int nv = p.Ep / 8, rows = 256 / nv;       // 16-byte columns, row lanes
+  // the block's first ids are on their way while the counts are summed
+  const int64_t first = (int64_t)blockIdx.x * p.tpb, t_end = min(p.T, first + p.tpb);
+  {
+    const int ns = (int)min((int64_t)ROUTE_TG, t_end - first) * p.topk;
+    for (int s = tid; s < ns; s += nthr) ids[s] = p.ids[first * p.topk + s];
+  }
+  const int nv = p.Ep / 8, rows = nthr / nv;       // 16-byte columns, row lanes
   const int col = tid % nv, r0 = tid / nv;
   if (r0 < rows) {
     int tot[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bef[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
     for (int b = r0; b < p.nblk; b += rows) {
       const v4i x = *(const v4i *)(p.counts + (int64_t)b * p.Ep + col * 8);
       const bool before = b < (int)blockIdx.x;
@@ -323,12 +576,13 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs p) {
   }
   __syncthreads();
   route_bases(p, pl);
-  const int64_t t_end = min(p.T, ((int64_t)blockIdx.x + 1) * p.tpb);
-  for (int64_t t0 = (int64_t)blockIdx.x * p.tpb; t0 < t_end; t0 += ROUTE_TG) {
+  for (int64_t t0 = first; t0 < t_end; t0 += ROUTE_TG) {
     const int ns = (int)min((int64_t)ROUTE_TG, t_end - t0) * p.topk;
-    __syncthreads();
-    for (int s = tid; s < ns; s += 256) ids[s] = p.ids[t0 * p.topk + s];
-    __syncthreads();
+    if (t0 != first) {
+      __syncthreads();
+      for (int s = tid; s < ns; s += nthr) ids[s] = p.ids[t0 * p.topk + s];
+      __syncthreads();
+    }
     route_mark(pl, ids, ns, p.topk, p.E);
     route_place(p, pl, ids, ns, t0);
   }
