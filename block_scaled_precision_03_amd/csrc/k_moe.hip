@@ -232,8 +232,9 @@ extern "C" int moe_combine_backward(const void *dout, const void *y, const float
   if (!dout || (!dy && rows > 0)) return MXG_ERR_INVALID_ARG;
   if (!aligned(dout, 16) || !aligned(dy, 16) || !aligned(dw, 4)) return MXG_ERR_MISALIGNED;
   CombineGradArgs a = {(const uint16_t *)dout, (const uint16_t *)y, w, row_of, (uint16_t *)dy, dw, T, N, rows, topk};
-  const int64_t blocks = cdiv(T * topk, 4);
-  hipLaunchKernelGGL(N % 8 == 0 ? combine_backward_kernel<8> : combine_backward_kernel<1>, dim3((unsigned)blocks),
-                     dim3(256), 0, stream, a);
+  const bool vec = N % 8 == 0;
+  const unsigned threads = (unsigned)std::min<int64_t>(256, cdiv(cdiv(N, vec ? 8 : 1), 64) * 64);
+  hipLaunchKernelGGL(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>, dim3((unsigned)T), dim3(threads), 0,
+                     stream, a);
   return launch_status();
 }

@@ -107,7 +107,10 @@ struct OpMax {
   __device__ double operator()(double a, double b) const { return fmax(a, b); }
   __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-struct OpAdd { __device__ double operator()(double a, double b) const { return a + b; } };
+struct OpAdd {
+  __device__ double operator()(double a, double b) const { return a + b; }
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
 struct OpMin {
   __device__ int operator()(int a, int b) const { return min(a, b); }
   __device__ float operator()(float a, float b) const { return fminf(a, b); }
@@ -606,16 +609,8 @@ struct RouteGradArgs {
   float scale;
 };
 
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
-  return x;
-}
-__device__ inline float wave_max(float x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
-  return x;
-}
+__device__ inline float wave_sum(float x) { return lanes_reduce<64>(x, OpAdd()); }
+__device__ inline float wave_max(float x) { return lanes_reduce<64>(x, OpMax()); }
 
 // A logit's finite stand-in; -inf where the expert is not available (-inf
 // or NaN).
@@ -680,8 +675,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
     mine = id >= 0 ? c * ex * s1 * s1 : 0.0f;
   }
   for (int r = 0; r < p.topk; ++r) {
-    const int e = __shfl(id, r, 64);
-    const float g = __shfl(mine, r, 64);
+    const int e = __builtin_amdgcn_readlane(id, r);
+    const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), r));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) ds[j] = e == lane + 64 * j ? g : ds[j];
   }
@@ -808,12 +803,12 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(QuantArgs p) {
   const float inv = 1.0f / s;
   auto put = [&](int c, const v4i &q) {
     if (p.row_of == nullptr) {
-      *(v4i *)(p.codes + t * p.K + 16 * c) = q;
+      __builtin_nontemporal_store(q, (v4i *)(p.codes + t * p.K + 16 * c));
       return;
     }
     for (int k = 0; k < p.topk; ++k) {
       const int64_t r = p.row_of[t * p.topk + k];
-      if (r >= 0 && r < p.T * p.topk) *(v4i *)(p.codes + r * p.K + 16 * c) = q;
+      if (r >= 0 && r < p.T * p.topk) __builtin_nontemporal_store(q, (v4i *)(p.codes + r * p.K + 16 * c));
     }
   };
 #pragma unroll
@@ -861,14 +856,14 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < p.topk; ++k) {
     const int64_t r = p.row_of[t * p.topk + k];
     if (r < 0 || r >= p.rows) continue;
     const float w = p.w[t * p.topk + k];
     const uint16_t *src = p.y + r * p.N + c;
     if constexpr (VEC == 8) {
-      const v4i u = *(const v4i *)src;
+      const v4i u = __builtin_nontemporal_load((const v4i *)src);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[2 * i] = fmaf(w, __uint_as_float((uint32_t)u[i] << 16), acc[2 * i]);
@@ -883,7 +878,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
     v4i o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = (int)pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
-    *(v4i *)dst = o;
+    __builtin_nontemporal_store(o, (v4i *)dst);
   } else {
     store_elem(dst, acc[0]);
   }
@@ -899,46 +894,72 @@ struct CombineGradArgs {
   int topk;
 };
 
-// One wave per (token, slot): its row of y and the token's row of dout
-// (shared through the caches by the token's slots) in, its row of dy out,
-// the dot product in registers and one wave reduction.
+// One workgroup (up to four waves) per token: its row of dout stays in
+// registers for eight slots at a time, whose rows of y are in flight
+// together; the dot products end in a wave reduction and one sum over the
+// waves.  With a wave per (token, slot) instead, dout came from the caches
+// once per slot: 2049 tokens x 8 x 4096 62.1 us.
 template <int VEC>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t s = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (s >= p.T * p.topk) return;
-  const int64_t t = s / p.topk;
-  const int64_t r = p.row_of[s];
-  if (r < 0 || r >= p.rows) {
-    if (lane == 0) p.dw[s] = 0.0f;
-    return;
-  }
-  const float w = p.w[s];
-  const uint16_t *d = p.dout + t * p.N, *y = p.y + r * p.N;
-  uint16_t *o = p.dy + r * p.N;
-  float acc = 0.0f;
-#pragma unroll 4
-  for (int64_t c = lane * VEC; c < p.N; c += 64 * VEC) {
-    if constexpr (VEC == 8) {
-      const v4i a = *(const v4i *)(d + c), b = *(const v4i *)(y + c);
-      v4i g;
+  constexpr int S = 8;
+  __shared__ float part[4][S];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = (int)blockDim.x >> 6;
+  const int64_t t = blockIdx.x;
+  const uint16_t *d = p.dout + t * p.N;
+  for (int k0 = 0; k0 < p.topk; k0 += S) {
+    int64_t row[S];                      // -1: no row
+    float w[S], acc[S];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = __uint_as_float((uint32_t)a[i] << 16), a1 = __uint_as_float((uint32_t)a[i] & 0xFFFF0000u);
-        const float b0 = __uint_as_float((uint32_t)b[i] << 16), b1 = __uint_as_float((uint32_t)b[i] & 0xFFFF0000u);
-        acc = fmaf(a0, b0, acc);
-        acc = fmaf(a1, b1, acc);
-        g[i] = (int)pack_bf16x2(w * a0, w * a1);
-      }
-      *(v4i *)(o + c) = g;
-    } else {
-      const float a0 = bf16_to_f32(d[c]);
-      acc = fmaf(a0, bf16_to_f32(y[c]), acc);
-      store_elem(o + c, w * a0);
+    for (int k = 0; k < S; ++k) {
+      const bool in = k0 + k < p.topk;
+      const int64_t s = t * p.topk + (in ? k0 + k : 0), r = p.row_of[s];
+      row[k] = in && r >= 0 && r < p.rows ? r : -1;
+      w[k] = p.w[s];
+      acc[k] = 0.0f;
     }
+    for (int64_t c = (int64_t)tid * VEC; c < p.N; c += (int64_t)blockDim.x * VEC) {
+      if constexpr (VEC == 8) {
+        const v4i a = *(const v4i *)(d + c);
+        v4i y[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k)
+          y[k] = row[k] >= 0 ? __builtin_nontemporal_load((const v4i *)(p.y + row[k] * p.N + c)) : (v4i){0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+          if (row[k] < 0) continue;
+          v4i g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a0 = __uint_as_float((uint32_t)a[i] << 16), a1 = __uint_as_float((uint32_t)a[i] & 0xFFFF0000u);
+            acc[k] = fmaf(a0, __uint_as_float((uint32_t)y[k][i] << 16), acc[k]);
+            acc[k] = fmaf(a1, __uint_as_float((uint32_t)y[k][i] & 0xFFFF0000u), acc[k]);
+            g[i] = (int)pack_bf16x2(w[k] * a0, w[k] * a1);
+          }
+          __builtin_nontemporal_store(g, (v4i *)(p.dy + row[k] * p.N + c));
+        }
+      } else {
+        const float a0 = bf16_to_f32(d[c]);
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+          if (row[k] < 0) continue;
+          acc[k] = fmaf(a0, bf16_to_f32(p.y[row[k] * p.N + c]), acc[k]);
+          store_elem(p.dy + row[k] * p.N + c, w[k] * a0);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const float sum = wave_sum(acc[k]);
+      if (lane == 0) part[wave][k] = sum;
+    }
+    __syncthreads();
+    if (tid < S && k0 + tid < p.topk) {
+      float sum = part[0][tid];
+      for (int v = 1; v < waves; ++v) sum += part[v][tid];
+      p.dw[t * p.topk + k0 + tid] = sum;
+    }
+    __syncthreads();
   }
-  acc = wave_sum(acc);
-  if (lane == 0) p.dw[s] = acc;
 }
 
 }  // namespace mxg
