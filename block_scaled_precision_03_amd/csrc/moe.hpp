@@ -289,6 +289,43 @@ __device__ inline int choose64(const RouteArgs &p, const IN *row, const LaneSpan
   return id;
 }
 
+// How many groups come before the lane's by 64-bit values of the lane's best
+// three experts (by v, its 32-bit choice values); `open` where its fourth is
+// too close to its second to leave it out.
+template <class IN, int LPT, int VPT, class Apart>
+__device__ inline int groups64(const RouteArgs &p, const IN *row, const LaneSpan &sp, const float (&v)[VPT],
+                               Apart apart, bool &open) {
+  const float NONE = -__builtin_inff();
+  float a[4] = {NONE, NONE, NONE, NONE};
+  int at[3] = {0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const float x = v[j];
+    const bool b0 = x > a[0], b1 = x > a[1], b2 = x > a[2];
+    a[3] = b2 ? a[2] : fmaxf(a[3], x);
+    at[2] = b1 ? at[1] : (b2 ? j : at[2]);
+    a[2] = b1 ? a[1] : (b2 ? x : a[2]);
+    at[1] = b0 ? at[0] : (b1 ? j : at[1]);
+    a[1] = b0 ? a[0] : (b1 ? x : a[1]);
+    at[0] = b0 ? j : at[0];
+    a[0] = b0 ? x : a[0];
+  }
+  open = p.bias && !apart(a[1], a[3]);
+  double g1 = -__builtin_inf(), g2 = g1;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (a[k] > NONE) {
+      const int e = sp.e0 + at[k];
+      const double x = logistic((double)fin(load_elem(row + e))) + (p.bias ? (double)p.bias[e] : 0.0);
+      g2 = fmax(g2, fmin(g1, x));
+      g1 = fmax(g1, x);
+    }
+  }
+  group_best(p, g1, g2);
+  const bool top2 = p.group_score == MOE_GROUP_TOP2;
+  return group_rank<LPT>(p, top2 && g2 > -__builtin_inf() ? g1 + g2 : g1, sp.gi);
+}
+
 // The choice from values in 32 bits, where they can decide it.  Without a
 // bias they are the logits themselves.  A sigmoid's score plus bias is within
 // 4e-7 + 6e-8 |value| of the exact sum (the exponential and the reciprocal
@@ -297,8 +334,9 @@ __device__ inline int choose64(const RouteArgs &p, const IN *row, const LaneSpan
 // experts by 32 bits hold the topk best wherever the topk-th is so far from
 // the first one left, and 64-bit values of these candidates alone, one per
 // lane, give the choice and its order.  Groups are decided by 32 bits where
-// the last kept and the first dropped are far enough apart.  `open` is set
-// where this does not decide (about one token in 5000), for choose64.
+// the last kept and the first dropped are far enough apart, else by groups64.
+// `open` is set where this does not decide, for choose64: that takes several
+// values within 1e-6 of each other at one border.
 // 16384 tokens of 256 experts in 8 groups, 8 chosen by sigmoid and bias: 35 us
 // with all values in 64 bits.
 template <class IN, int LPT, int VPT>
@@ -332,11 +370,11 @@ __device__ inline int choose32(const RouteArgs &p, const IN *row, const LaneSpan
   if (p.n_group > 1) {
     group_best(p, g1, g2);
     const float gs = top2 && g2 > NONE ? g1 + g2 : g1;
-    const bool out = group_rank<LPT>(p, gs, sp.gi) >= p.topk_group;
+    bool out = group_rank<LPT>(p, gs, sp.gi) >= p.topk_group;
     if (p.bias || top2) {
       const float kept = lanes_reduce<LPT>(out ? -NONE : gs, OpMin());
       const float left = lanes_reduce<LPT>(out ? gs : NONE, OpMax());
-      open = !apart(kept, left);
+      if (__any(!apart(kept, left))) out = groups64<IN, LPT, VPT>(p, row, sp, v, apart, open) >= p.topk_group;
     }
     if (out) {
 #pragma unroll
@@ -552,16 +590,16 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
     const int ns = (int)min((int64_t)ROUTE_TG, t_end - first) * p.topk;
     for (int s = tid; s < ns; s += nthr) ids[s] = p.ids[first * p.topk + s];
   }
-  const int nv = p.Ep / 8, rows = nthr / nv;       // 16-byte columns, row lanes
+  const int nv = p.Ep / 4, rows = nthr / nv;       // columns of four experts, row lanes
   const int col = tid % nv, r0 = tid / nv;
   if (r0 < rows) {
-    int tot[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bef[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    int tot[4] = {0, 0, 0, 0}, bef[4] = {0, 0, 0, 0};
 #pragma unroll 8
     for (int b = r0; b < p.nblk; b += rows) {
-      const v4i x = *(const v4i *)(p.counts + (int64_t)b * p.Ep + col * 8);
+      const v2i x = *(const v2i *)(p.counts + (int64_t)b * p.Ep + col * 4);
       const bool before = b < (int)blockIdx.x;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const int lo = x[k] & 0xFFFF, hi = (uint32_t)x[k] >> 16;
         tot[2 * k] += lo;
         tot[2 * k + 1] += hi;
@@ -570,10 +608,10 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
       }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (col * 8 + k < p.E) {
-        atomicAdd(&pl.total[col * 8 + k], tot[k]);
-        atomicAdd(&pl.base[col * 8 + k], bef[k]);
+    for (int k = 0; k < 4; ++k) {
+      if (col * 4 + k < p.E) {
+        atomicAdd(&pl.total[col * 4 + k], tot[k]);
+        atomicAdd(&pl.base[col * 4 + k], bef[k]);
       }
     }
   }
