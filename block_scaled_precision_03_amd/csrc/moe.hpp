@@ -228,21 +228,21 @@ __device__ inline int group_rank(const RouteArgs &p, T gs, int gi) {
 
 // One rank of the choice: the largest value over the lanes, then the lowest
 // expert that holds it, which becomes NaN (no maximum takes it); -1: none.
+// (Where `at` is past a lane's experts it names a value that is -inf.)
 template <int LPT, int VPT, class T>
-__device__ inline int take_best(T (&v)[VPT], int e0, int cnt, T &best) {
+__device__ inline int take_best(T (&v)[VPT], int e0, T &best) {
   T bv = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < VPT; ++j) bv = fmax(bv, v[j]);
   bv = lanes_reduce<LPT>(bv, OpMax());
-  int be = 0x7FFFFFFF;
+  int jl = 0x7FFF;
 #pragma unroll
-  for (int j = VPT - 1; j >= 0; --j) be = v[j] == bv ? e0 + j : be;
-  be = lanes_reduce<LPT>(be, OpMin());
+  for (int j = VPT - 1; j >= 0; --j) jl = v[j] == bv ? j : jl;
+  const int be = lanes_reduce<LPT>(jl < VPT ? e0 + jl : 0x7FFFFFFF, OpMin());
   best = bv;
   const int chosen = bv > -__builtin_inff() ? be : -1, at = chosen - e0;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
-    if (at == j && j < cnt) v[j] = __builtin_nanf("");
+  for (int j = 0; j < VPT; ++j) v[j] = at == j ? (T)__builtin_nanf("") : v[j];
   return chosen;
 }
 
@@ -283,7 +283,7 @@ __device__ inline int choose64(const RouteArgs &p, const IN *row, const LaneSpan
   int id = -1;
   for (int r = 0; r < p.topk; ++r) {
     double best;
-    const int c = take_best<LPT>(v, sp.e0, sp.cnt, best);
+    const int c = take_best<LPT>(v, sp.e0, best);
     if (sub == r) id = c;
   }
   return id;
@@ -384,13 +384,13 @@ __device__ inline int choose32(const RouteArgs &p, const IN *row, const LaneSpan
   int id = -1;
   float last = NONE, next;
   for (int r = 0; r < p.topk; ++r) {
-    const int c = take_best<LPT>(v, sp.e0, sp.cnt, last);
+    const int c = take_best<LPT>(v, sp.e0, last);
     if (sub == r) id = c;
   }
   if (!p.bias) return id;
   int cand = p.topk;
   if (cand < LPT) {
-    const int c = take_best<LPT>(v, sp.e0, sp.cnt, next);
+    const int c = take_best<LPT>(v, sp.e0, next);
     if (sub == cand) id = c;
     ++cand;
   }
@@ -594,8 +594,12 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
   const int col = tid % nv, r0 = tid / nv;
   if (r0 < rows) {
     int tot[4] = {0, 0, 0, 0}, bef[4] = {0, 0, 0, 0};
+    // every block starts at its own row: in step they would read one row of
+    // counts, one L2 channel, at a time
+    const int turn = (int)blockIdx.x;
 #pragma unroll 8
-    for (int b = r0; b < p.nblk; b += rows) {
+    for (int i = r0; i < p.nblk; i += rows) {
+      const int b = i + turn < p.nblk ? i + turn : i + turn - p.nblk;
       const v2i x = *(const v2i *)(p.counts + (int64_t)b * p.Ep + col * 4);
       const bool before = b < (int)blockIdx.x;
 #pragma unroll
