@@ -134,11 +134,18 @@ extern "C" int moe_route(int dtype, const void *logits, const float *bias, int32
   if (!fits) return MXG_ERR_UNSUPPORTED;
   a.lpg = s.lpg;
   a.per = s.per;
-  // up to 16 waves, so that a block's 64 tokens run at once
-  const int64_t per_block = std::min<int64_t>(T, ROUTE_TG);
+  // A block of the choice: the tokens of a row of counts (64 wherever they
+  // give every compute unit a row), 32 of them where that leaves half of the
+  // compute units idle (256 experts, 8 chosen: a block of 64 tokens takes 13.2
+  // us, one of 32 takes 8.2), and 16 without maps; up to 16 waves, so that its
+  // tokens run at once.
+  a.halves = maps && !one && a.tpb == ROUTE_TG && 2 * a.nblk <= cu_count();
+  a.tpc = !maps ? 16 : a.halves ? ROUTE_TG / 2 : a.tpb;
+  const unsigned blocks = (unsigned)(!maps ? cdiv(T, 16) : a.halves ? 2 * a.nblk : a.nblk);
+  const int64_t per_block = std::min<int64_t>(std::min<int64_t>(T, ROUTE_TG), a.tpc);
   const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(256, cdiv(per_block * s.lpt, 64) * 64));
   route_fn fn = dtype == MXG_BF16 ? pick_route<uint16_t>(s, maps, one) : pick_route<float>(s, maps, one);
-  hipLaunchKernelGGL(fn, dim3((unsigned)a.nblk), dim3((unsigned)threads), 0, stream, a);
+  hipLaunchKernelGGL(fn, dim3(blocks), dim3((unsigned)threads), 0, stream, a);
   if (maps && !one) hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)a.nblk), dim3(a.nblk > 32 ? 1024 : 256), 0, stream, a);
   return launch_status();
 }

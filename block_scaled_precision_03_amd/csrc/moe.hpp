@@ -32,7 +32,9 @@ struct RouteArgs {
   int32_t *row_of, *slot_of;             // null: no maps
   uint16_t *counts;                      // [blocks][Ep]: rows of each expert by block
   int Ep, nblk;
-  int64_t tpb;                           // tokens per block, a multiple of ROUTE_TG
+  int64_t tpb;                           // tokens per row of counts, a multiple of ROUTE_TG
+  int64_t tpc;                           // tokens per block of the choice: tpb, or half of it
+  bool halves;                           // a count is the sum of two bytes, one per block of the choice
 };
 
 // LDS of the placement: which tokens of a group of 64 chose each expert.
@@ -537,11 +539,11 @@ __global__ void route_kernel(RouteArgs p) {
   __shared__ RoutePlace pl;
   const int tid = threadIdx.x, sub = tid & (LPT - 1);
   const int per_pass = blockDim.x / LPT;
-  const int64_t t_end = min(p.T, ((int64_t)blockIdx.x + 1) * p.tpb);
+  const int64_t t_end = min(p.T, ((int64_t)blockIdx.x + 1) * p.tpc);
   if constexpr (MAPS) {
     for (int e = tid; e < p.E; e += blockDim.x) pl.total[e] = pl.base[e] = 0;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * p.tpb; t0 < t_end; t0 += ROUTE_TG) {
+  for (int64_t t0 = (int64_t)blockIdx.x * p.tpc; t0 < t_end; t0 += ROUTE_TG) {
     const int nt = (int)min((int64_t)ROUTE_TG, t_end - t0);
     for (int tb = 0; tb < nt; tb += per_pass) {
       const int tl = tb + tid / LPT;
@@ -568,7 +570,10 @@ __global__ void route_kernel(RouteArgs p) {
     }
   }
   if constexpr (MAPS && !ONE) {
-    for (int e = tid; e < p.E; e += blockDim.x) p.counts[(int64_t)blockIdx.x * p.Ep + e] = (uint16_t)pl.total[e];
+    for (int e = tid; e < p.E; e += blockDim.x) {
+      if (p.halves) ((uint8_t *)p.counts)[((int64_t)(blockIdx.x >> 1) * p.Ep + e) * 2 + (blockIdx.x & 1)] = (uint8_t)pl.total[e];
+      else p.counts[(int64_t)blockIdx.x * p.Ep + e] = (uint16_t)pl.total[e];
+    }
   }
 }
 
@@ -604,7 +609,9 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
       const bool before = b < (int)blockIdx.x;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int lo = x[k] & 0xFFFF, hi = (uint32_t)x[k] >> 16;
+        const uint32_t u = (uint32_t)x[k];
+        const uint32_t c = p.halves ? (u & 0x00FF00FFu) + ((u >> 8) & 0x00FF00FFu) : u;
+        const int lo = (int)(c & 0xFFFF), hi = (int)(c >> 16);
         tot[2 * k] += lo;
         tot[2 * k + 1] += hi;
         bef[2 * k] += before ? lo : 0;
