@@ -102,7 +102,8 @@ extern "C" int mxgemm_init(void) {
   if (hipFuncGetAttributes(&attr, (const void *)pick_dense_mx_a4(F_E4M3, MXG_NT, false, false)) != hipSuccess)
     return MXG_ERR_HIP;
   (void)cu_count();
-  return int8_init();
+  const int v = int8_init();
+  return v == MXG_OK ? moe_init() : v;
 }
 
 extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,

@@ -42,5 +42,6 @@ int int8_dense_variant(int64_t M, int64_t N, int64_t K);
 int int8_run(const void *A, const void *sA, const void *B, const void *sB, void *D, int64_t M, int64_t N,
              int64_t K, const void *bias, int act, hipStream_t stream);
 int int8_init();
+int moe_init();                          // k_moe.hip
 
 }  // namespace mxg

@@ -6,6 +6,13 @@
 #include "host.hpp"
 #include "moe.hpp"
 
+namespace mxg {
+int moe_init() {
+  hipFuncAttributes attr;
+  return hipFuncGetAttributes(&attr, (const void *)route_place_kernel) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
+}
+}  // namespace mxg
+
 using namespace mxg;
 
 static_assert(MOE_SOFTMAX == MXG_MOE_SOFTMAX && MOE_SIGMOID == MXG_MOE_SIGMOID && MOE_GROUP_MAX == MXG_MOE_GROUP_MAX &&
@@ -158,16 +165,18 @@ extern "C" int moe_route_backward(int dtype, const void *logits, const int32_t *
   if (T == 0) return MXG_OK;
   if (!logits || !ids || !grad || !dlogits) return MXG_ERR_INVALID_ARG;
   if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(ids, 4) || !aligned(grad, 4)) return MXG_ERR_MISALIGNED;
-  RouteGradArgs a = {logits, ids, grad, dlogits, T, (int)E, topk, score, renormalize != 0, scale};
-  const unsigned grid = (unsigned)cdiv(T, 4);
+  const bool four = E <= 256 && topk <= 16;      // 16 lanes per token, four tokens per wave
+  const int lpt = four ? 16 : 64, per = (int)cdiv(E, lpt);
+  RouteGradArgs a = {logits, ids, grad, dlogits, T, (int)E, topk, score, renormalize != 0, scale, per};
   auto go = [&](auto in) {
     typedef decltype(in) IN;
-    void (*fn)(RouteGradArgs) = E <= 64    ? route_backward_kernel<IN, 1>
-                                : E <= 128 ? route_backward_kernel<IN, 2>
-                                : E <= 256 ? route_backward_kernel<IN, 4>
-                                : E <= 512 ? route_backward_kernel<IN, 8>
-                                           : route_backward_kernel<IN, 16>;
-    hipLaunchKernelGGL(fn, dim3(grid), dim3(256), 0, stream, a);
+    void (*fn)(RouteGradArgs) = four ? (per <= 4   ? route_backward_kernel<IN, 16, 4>
+                                        : per <= 8 ? route_backward_kernel<IN, 16, 8>
+                                                   : route_backward_kernel<IN, 16, 16>)
+                                     : (per <= 4   ? route_backward_kernel<IN, 64, 4>
+                                        : per <= 8 ? route_backward_kernel<IN, 64, 8>
+                                                   : route_backward_kernel<IN, 64, 16>);
+    hipLaunchKernelGGL(fn, dim3((unsigned)cdiv(T, 256 / lpt)), dim3(256), 0, stream, a);
   };
   if (dtype == MXG_BF16) go((uint16_t)0);
   else go(0.0f);
