@@ -778,7 +778,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
 // below 2^-96 or above 2^96 divide.
 //
 // A stream: 4096 x 14336 BF16 in 34.4 us (5.1 TB/s), 2049 x 7168 to eight rows
-// each in 24.5 (6.0 TB/s); the codes bypass the caches (36.3 and 30.2 through
+// each in 27.0 (5.5 TB/s); the codes bypass the caches (36.3 and 30.2 through
 // them), x does not (bypassing cost 2 %).
 struct QuantArgs {
   const void *x;
