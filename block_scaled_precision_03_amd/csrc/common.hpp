@@ -201,6 +201,11 @@ __device__ inline float activate(int act, float z) {
   return z;
 }
 
+// Workgroup index of a grid that the host folds into rows of 2^20 (flat_grid):
+// a dimension holds fewer than 2^32 work-items.
+constexpr int FLAT_LOG2 = 20;
+__device__ inline int64_t flat_block() { return ((int64_t)blockIdx.y << FLAT_LOG2) + blockIdx.x; }
+
 __device__ inline uint32_t lds_load_u32(const void *p) { return *(const lds_u32_t *)p; }
 
 }  // namespace mxg

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/mxgemm.h"
+#include "common.hpp"
 
 namespace mxg {
 
@@ -18,6 +19,12 @@ inline int launch_status() {
 }
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A grid of at least n workgroups for kernels that use flat_block().
+inline dim3 flat_grid(int64_t n) {
+  const int64_t row = 1ll << FLAT_LOG2;
+  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)cdiv(n, row));
+}
 
 // Compute units of the current device: the grid size of the persistent
 // kernels.  Queried once per device.

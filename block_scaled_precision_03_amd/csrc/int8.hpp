@@ -757,7 +757,7 @@ __global__ void int8_fill_kernel(Int8Args p) {
       covered += s < 0 ? 0 : (s > room ? room : s);
     }
   }
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = flat_block() * 256 + threadIdx.x;
   if (i >= covered * p.No) return;
   const int64_t c = i % p.No;
   auto bias = [&](int64_t n) { return p.bias ? __uint_as_float((uint32_t)p.bias[n] << 16) : 0.0f; };

@@ -71,7 +71,7 @@ int launch(Int8Args &a, hipStream_t stream) {
   if (a.K == 0) {
     const int64_t blocks = cdiv(a.M * a.No, 256);
     if (blocks > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(int8_fill_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(int8_fill_kernel, flat_grid(blocks), dim3(256), 0, stream, a);
     return launch_status();
   }
   const Kernel k = choose(a.G, a.M, a.N, a.K);

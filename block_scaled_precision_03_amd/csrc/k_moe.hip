@@ -202,7 +202,7 @@ extern "C" int mxgemm_quantize_int8(int dtype, const void *x, void *codes, float
                             : K <= 8192  ? quant_int8_kernel<IN, 256, 2, false>
                             : K <= 16384 ? quant_int8_kernel<IN, 256, 4, false>
                                          : quant_int8_kernel<IN, 256, 4, true>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)(K <= 4096 ? cdiv(T, 4) : T)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(fn, flat_grid(K <= 4096 ? cdiv(T, 4) : T), dim3(256), 0, stream, a);
   };
   if (dtype == MXG_BF16) go((uint16_t)0);
   else go(0.0f);
@@ -250,7 +250,7 @@ extern "C" int moe_combine_backward(const void *dout, const void *y, const float
   CombineGradArgs a = {(const uint16_t *)dout, (const uint16_t *)y, w, row_of, (uint16_t *)dy, dw, T, N, rows, topk};
   const bool vec = N % 8 == 0;
   const unsigned threads = (unsigned)std::min<int64_t>(256, cdiv(cdiv(N, vec ? 8 : 1), 64) * 64);
-  hipLaunchKernelGGL(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>, dim3((unsigned)T), dim3(threads), 0,
+  hipLaunchKernelGGL(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>, flat_grid(T), dim3(threads), 0,
                      stream, a);
   return launch_status();
 }

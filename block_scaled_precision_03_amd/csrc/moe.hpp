@@ -848,8 +848,8 @@ template <class IN, int GROUP, int NV, bool WIDE>
 __global__ __launch_bounds__(256) void quant_int8_kernel(QuantArgs p) {
   __shared__ float part[4];
   const int tid = threadIdx.x, gl = tid & (GROUP - 1);
-  const int64_t t = (int64_t)blockIdx.x * (256 / GROUP) + tid / GROUP;
-  if (GROUP == 64 && t >= p.T) return;
+  const int64_t t = flat_block() * (256 / GROUP) + tid / GROUP;
+  if (t >= p.T) return;                  // GROUP 256: the whole workgroup
   const IN *row = (const IN *)p.x + t * p.K;
   const int np = (int)(p.K / 16);
   Piece<IN> x[NV];
@@ -985,7 +985,8 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradArgs p
   constexpr int S = 8;
   __shared__ float part[4][S];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = (int)blockDim.x >> 6;
-  const int64_t t = blockIdx.x;
+  const int64_t t = flat_block();
+  if (t >= p.T) return;
   const uint16_t *d = p.dout + t * p.N;
   for (int k0 = 0; k0 < p.topk; k0 += S) {
     int64_t row[S];                      // -1: no row

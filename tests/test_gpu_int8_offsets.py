@@ -79,3 +79,24 @@ def test_quantize_and_combine_far_rows():
         ref = float(2 * (x[r].double() ** 2).sum())
         # FP32 sums of K products, each partial sum rounded once
         assert abs(float(dw[T - 1 - r]) - ref) <= ref * K * 2.0 ** -24
+
+
+def test_more_workgroups_than_one_dimension_holds():
+    """Grids of 2^32 work-items and more."""
+    m = _mx()
+    T = (1 << 26) + 5                              # a wave per row
+    x = torch.zeros(T, 16, dtype=torch.bfloat16, device=DEV)
+    x[-1] = torch.arange(112, 128, device=DEV).bfloat16()
+    q, s = torch.empty(T, 16, dtype=torch.int8, device=DEV), torch.zeros(T, device=DEV)
+    m.quantize_int8(m.BF16, x, q, s, T, 16)
+    assert bool((s == 1).all()) and torch.equal(q[-1].float(), x[-1].float()) and not bool(q[:-1].any())
+    T = (1 << 24) + 5                              # a workgroup per token
+    d = torch.zeros(T, 2048, dtype=torch.bfloat16, device=DEV)
+    d[-1] = 3
+    row_of = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1)
+    w, dw, dy = torch.full((T, 1), 2.0, device=DEV), torch.full((T, 1), 9.0, device=DEV), torch.empty_like(d)
+    m.moe_combine_backward(d, d, w, row_of, dy, dw, T, 1, 2048, T)
+    assert bool((dy[-1] == 6).all()) and float(dw[-1]) == 9.0 * 2048 and not bool(dw[:-1].any())
+    D = torch.full((70000, 65536), 7, dtype=torch.bfloat16, device=DEV)   # a value each
+    m.run(m.INT8, m.INT8, m.NT, None, None, None, None, D, 70000, 65536, 0)
+    assert not bool(D[0].any()) and not bool(D[-1].any()) and not bool(D[65536:65540].any())
