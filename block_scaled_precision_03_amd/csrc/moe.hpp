@@ -681,7 +681,8 @@ __device__ inline void store4(uint16_t *p, const float *v) {
 
 template <class IN, int LPT, int VPT>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
-  __shared__ float share[256 / LPT][LPT * VPT];
+  // expert j of lane i at j LPT + i, tokens 16 banks apart: no conflicts
+  __shared__ float share[256 / LPT][LPT * VPT + 16];
   const int tid = threadIdx.x, sub = tid & (LPT - 1);
   const int64_t tw = (int64_t)blockIdx.x * (256 / LPT) + tid / LPT;
   const bool live = tw < p.T;
@@ -695,7 +696,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     l[j] = avail_logit(l[j]);
-    mine_row[sub * VPT + j] = 0.0f;
+    mine_row[j * LPT + sub] = 0.0f;
   }
   // lane r holds choice r
   int id = -1;
@@ -742,7 +743,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
     mine = id >= 0 ? c * ex * s1 * s1 : 0.0f;
   }
   __syncthreads();
-  if (id >= 0) mine_row[id / p.per * VPT + id % p.per] = mine;
+  if (id >= 0) mine_row[id % p.per * LPT + id / p.per] = mine;
   __syncthreads();
   if (!live) return;
   IN *drow = (IN *)p.dlogits + t * p.E + e0;
@@ -751,7 +752,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs p) {
     float d[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      d[k] = mine_row[sub * VPT + j + k];
+      d[k] = mine_row[(j + k) * LPT + sub];
       if (!p.renorm && sm) d[k] = l[j + k] > 0.0f ? l[j + k] * inv * (d[k] - dot) : 0.0f;
     }
     if (j + 4 <= cnt) {
