@@ -336,7 +336,10 @@ __device__ inline int groups64(const RouteArgs &p, const IN *row, const LaneSpan
 // experts by 32 bits hold the topk best wherever the topk-th is so far from
 // the first one left, and 64-bit values of these candidates alone, one per
 // lane, give the choice and its order.  Groups are decided by 32 bits where
-// the last kept and the first dropped are far enough apart, else by groups64.
+// every kept one stays before every dropped one whatever their errors, else by
+// groups64; the error of a sum of two is that of its terms, which may be far
+// larger than the sum: 8e-7 + 1.2e-7 (|g1| + |g2|), and a rounding more for
+// the interval's ends.
 // `open` is set where this does not decide, for choose64: that takes several
 // values within 1e-6 of each other at one border.
 // 16384 tokens of 256 experts in 8 groups, 8 chosen by sigmoid and bias: the
@@ -374,9 +377,13 @@ __device__ inline int choose32(const RouteArgs &p, const IN *row, const LaneSpan
     const float gs = top2 && g2 > NONE ? g1 + g2 : g1;
     bool out = group_rank<LPT>(p, gs, sp.gi) >= p.topk_group;
     if (p.bias || top2) {
-      const float kept = lanes_reduce<LPT>(out ? -NONE : gs, OpMin());
-      const float left = lanes_reduce<LPT>(out ? gs : NONE, OpMax());
-      if (__any(!apart(kept, left))) out = groups64<IN, LPT, VPT>(p, row, sp, v, apart, open) >= p.topk_group;
+      const bool some = g1 > NONE;       // else no available expert: comes last
+      const float err = 8e-7f + 2.5e-7f * (fabsf(g1) + (top2 && g2 > NONE ? fabsf(g2) : 0.0f));
+      const bool known = err < -NONE;    // the sum is in 32-bit range
+      const float lo = some && known ? gs - err : NONE, hi = some ? (known ? gs + err : -NONE) : NONE;
+      const float kept = lanes_reduce<LPT>(out ? -NONE : lo, OpMin());
+      const float left = lanes_reduce<LPT>(out ? hi : NONE, OpMax());
+      if (__any(left > NONE && !(kept > left))) out = groups64<IN, LPT, VPT>(p, row, sp, v, apart, open) >= p.topk_group;
     }
     if (out) {
 #pragma unroll
