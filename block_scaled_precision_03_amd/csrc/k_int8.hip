@@ -22,38 +22,55 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
 // through LDS in 64 x 64 or 128 x 128 tiles, 256 x 256 tiles.
 enum Kernel { ROWS16, ROWS32, STREAM64, STREAM128, TILED };
 
+// Row tiles of b rows that a call can have at most: n groups that own rows
+// take n + (M - n) / b, which grows with n.
+int64_t max_row_tiles(int G, int64_t M, int b) {
+  const int64_t n = std::min<int64_t>(G, M);
+  return n + (M - n) / b;
+}
+
 // Estimated microseconds of each kernel, from static shapes alone (m_sizes
-// stays on the device: each group is taken to end inside a row tile).  The
-// constants are fitted to 122 dense and grouped calls of 1 .. 16384 rows, all
-// kernels timed on each; there the choice is the fastest kernel or within 14 %
-// of it, 0.9 % on average.  Both sides where the choice turns: 3 x 3829 x
-// 3984 takes 5.9 us in ROWS16 and 14.4 in STREAM64, 65 x 12000 x 4096 55 and
-// 17; 200 x 2000 x 400 5.3 in ROWS32 and 5.9 in STREAM64, 777 x 5002 x 4112
-// 84 and 49, 38 in STREAM128; 2049 x 8000 x 2064 68 in STREAM128 and 58 in
-// TILED, 6449 x 1003 x 1040 22 and 28.
+// stays on the device).  The rows are taken to fall on the groups at random:
+// `live` of them own rows, and each of those fills half of its last row tile
+// but at least one tile.  The constants are fitted to 170 dense calls of 1 ..
+// 16384 rows and 706 grouped ones of 2 .. 1024 groups and 1 .. 16384 rows (N 256
+// .. 28672, K 256 .. 14336), all kernels timed on each.  There the choice takes 1 % more than the fastest kernel on
+// average, over 14 % more in 1 of 100 calls and at most 29 %; on 420 more calls,
+// drawn afterwards, 1.4 %, over 14 % more in 11 and at most 42 %.  Both sides
+// where the choice turns, in us: 3 x 3829 x 3984 5.9 in ROWS16, 14.4 in STREAM64; 65 x
+// 12000 x 4096 55 and 17; 200 x 2000 x 400 5.3 in ROWS32, 5.9 in STREAM64; 777 x
+// 5002 x 4112 84 and 49, 38 in STREAM128; 2049 x 8000 x 2064 68 in STREAM128, 58
+// in TILED; 6449 x 1003 x 1040 22 and 28; 64 groups, 128 rows x 1536 x 4096 58 in
+// ROWS16, 64 in STREAM64, 109 in TILED; 256 groups, 256 rows x 4096 x 7168 808,
+// 738 and 1021; 8 groups, 1024 rows x 4608 x 7168 83 in STREAM128, 103 in TILED,
+// 2048 rows 120 and 105.
 Kernel choose(int G, int64_t M, int64_t N, int64_t K) {
   if (G < 1 || M <= 0 || N <= 0 || K <= 0) return STREAM64;
-  const double cus = cu_count(), nst = (double)cdiv(K, 128), live = (double)std::min<int64_t>(G, M);
-  auto tiles = [&](int b) { return (G == 1 ? (double)cdiv(M, b) : (double)M / b + 0.5 * live) * (double)cdiv(N, b); };
-  // memory: weights, activations and output once, 6.9 TB/s
-  const double mem = (live * (double)N * (double)K + (double)M * (double)K + 2.0 * (double)M * (double)N) / 6.9e6;
+  const double cus = cu_count(), nst = (double)cdiv(K, 128);
+  const double live = G == 1 ? 1.0 : G * (1.0 - std::pow(1.0 - 1.0 / G, (double)M));
+  auto tiles = [&](int b) {
+    return (G == 1 ? (double)cdiv(M, b) : std::max(live, (double)M / b + 0.5 * live)) * (double)cdiv(N, b);
+  };
+  // weights, activations and output once, at the rate of each kernel (TB/s)
+  const double bytes = live * (double)N * (double)K + (double)M * (double)K + 2.0 * (double)M * (double)N;
+  auto mem = [&](double rate) { return bytes / (rate * 1e6); };
   double t[5];
-  // ROWS: a compute unit's 36 (30) bytes per ns of operands, tiles of full rows
-  auto rows = [&](int b, double t0, double rate, double per_tile) {
-    const double n = tiles(b), bytes = (std::min((double)b, (double)M / live) + b) * (double)K;
-    return t0 + std::max(std::max(1.0, n / cus) * bytes / rate, mem) + per_tile * n / cus;
+  // ROWS: a compute unit's 31 (25) bytes per ns of operands, tiles of full rows
+  auto rows = [&](int b, double t0, double rate, double per_tile, double m) {
+    const double n = tiles(b), ops = (std::min((double)b, (double)M / live) + b) * (double)K;
+    return t0 + std::max(std::max(1.0, n / cus) * ops / rate, m) + per_tile * n / cus;
   };
-  t[ROWS16] = rows(16, 3.2, 35.9e3, 0.27);
-  t[ROWS32] = rows(32, 3.6, 29.7e3, 0.52);
+  t[ROWS16] = rows(16, 2.71, 30.7e3, 0.432, mem(5.52));
+  t[ROWS32] = rows(32, 3.15, 24.9e3, 0.788, mem(4.07));
   // STREAM: two workgroups per compute unit, a K step's time in a round of tiles
-  auto stream = [&](int b, double t0, double alone, double shared, double per_tile) {
+  auto stream = [&](int b, double t0, double alone, double shared, double per_tile, double m) {
     const double n = tiles(b), step = n <= cus ? alone : shared * std::ceil(n / (2 * cus));
-    return t0 + std::max(nst * step, mem) + per_tile * n / (2 * cus);
+    return t0 + std::max(nst * step, m) + per_tile * n / (2 * cus);
   };
-  t[STREAM64] = stream(64, 3.5, 0.36, 0.65, 0.6);
-  t[STREAM128] = stream(128, 4.3, 0.80, 1.31, 2.9);
+  t[STREAM64] = stream(64, 3.63, 0.401, 0.536, 1.10, mem(7.19));
+  t[STREAM128] = stream(128, 4.26, 0.81, 1.21, 1.39, mem(6.70));
   const double nt = tiles(DBM);
-  t[TILED] = 3.6 + std::ceil(nt / cus) * (nst * (nt <= cus ? 1.28 : 1.71) + 6.4);
+  t[TILED] = 5.03 + std::max(std::ceil(nt / cus) * (nst * (nt <= cus ? 1.44 : 1.57) + 4.22), mem(3.82));
   return (Kernel)(std::min_element(t, t + 5) - t);
 }
 
@@ -77,7 +94,7 @@ int launch(Int8Args &a, hipStream_t stream) {
   const Kernel k = choose(a.G, a.M, a.N, a.K);
   const int BT = k == ROWS16 ? 16 : k == ROWS32 ? 32 : k == STREAM64 ? 64 : k == STREAM128 ? 128 : DBM;
   a.tiles_n = (int)cdiv(a.N, BT);
-  const int64_t tiles = (cdiv(a.M, BT) + a.G - 1) * a.tiles_n;
+  const int64_t tiles = max_row_tiles(a.G, a.M, BT) * a.tiles_n;
   if (tiles > 0x7FFFFFF0) return MXG_ERR_UNSUPPORTED;
   void (*fn)(Int8Args);
   int64_t grid = 0;
