@@ -53,9 +53,20 @@ class Int8MoE:
         mx.quantize_int8(mx.F32 if w.dtype == torch.float32 else mx.BF16, w, q, s, E * N, K)
         return q, s
 
+    def _check(self, x, logits):
+        """The library takes addresses and sizes alone: what does not fit the
+        layer's buffers is refused here."""
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError("%d tokens, the layer has room for %d" % (T, self.max_tokens))
+        for t, shape, dtype in ((x, (T, self.D), torch.bfloat16), (logits, (T, self.E), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("expected a contiguous %s of %s, got %s of %s" % (dtype, shape, t.dtype, tuple(t.shape)))
+
     def forward(self, x, logits):
-        """x: BF16 [T, dim], logits: FP32 [T, experts]; returns BF16 [T, dim]
-        (a view of the layer's buffer)."""
+        """x: BF16 [T, dim], logits: FP32 [T, experts], T <= max_tokens;
+        returns BF16 [T, dim] (a view of the layer's buffer)."""
+        self._check(x, logits)
         T, E, k, D, F = x.shape[0], self.E, self.k, self.D, self.F
         n = T * k
         mx.moe_route(mx.F32, logits, None, self.ids, self.weights, T, E, k, m_sizes=self.sizes, row_of=self.row_of,
@@ -71,6 +82,7 @@ class Int8MoE:
     def backward(self, dout, logits):
         """Gradients after forward(x, logits): of the experts' outputs (BF16,
         in their rows' order) and of the logits."""
+        self._check(dout, logits)
         T, k, n = dout.shape[0], self.k, dout.shape[0] * self.k
         mx.moe_combine_backward(dout, self.y, self.weights, self.row_of, self.dy, self.dweights, T, k, self.D, n)
         mx.moe_route_backward(mx.F32, logits, self.ids, self.dweights, self.dlogits, T, self.E, k)
