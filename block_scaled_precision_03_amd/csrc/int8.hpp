@@ -111,13 +111,17 @@ __device__ inline void int8_columns(const Int8Args &p, int g, int64_t n0, int c,
 // x 64 per wave (8 x 4 matrix-core tiles, 128 integer accumulators), two LDS
 // stages of 128 bytes of K filled by DMA from waves 4-7 (each SIMD then has
 // one wave that starts on the matrix cores right after the barrier while its
-// other wave queues the DMAs), a persistent grid whose tiles share one
-// unbroken K pipeline, and a finished tile stored during the next tile's
-// first K step: the schedule that the block-scaled kernels measured best.
+// other wave queues the DMAs), a persistent grid whose tiles share one K
+// pipeline (an odd count of K steps drains it at the end of every tile: no
+// slower, 16384 x 14336 takes 24.2 us per 128 of K with 31, 32 and 33 steps), and
+// a finished tile stored during the next tile's first K step: the schedule that
+// the block-scaled kernels measured best.
 // The tile's 256 row scales, 256 channel scales and 256 biases come into LDS
 // with its first stage, in two slots by the tile's parity.  16384 x 14336 x 4096
-// takes 735 us, 2.6 POP/s; each compute unit's way into and out of its LDS
-// (64 KB in, 192 KB out per K step) holds it at half of the matrix cores' rate.
+// takes 735 to 790 us from run to run, 2.4 to 2.6 POP/s, about half of the
+// matrix cores' peak.  A K step moves 64 KB into and 192 KB out of a compute
+// unit's LDS: 2048 clocks at 128 bytes a clock, as long as its matrix cores take
+// for the step, and the two overlap in part.
 // The activation is a template argument: as a switch on a kernel argument,
 // repeated for each of the tile's 128 accumulators, it made 34 K instructions
 // with 216 scratch accesses (5.1 ms for M = 16384, N = 14336, K = 4096).

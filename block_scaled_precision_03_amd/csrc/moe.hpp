@@ -119,12 +119,13 @@ struct OpMin {
 };
 
 // e^-t for t >= 0 in 64 bits, within about an ulp: -t = n ln 2 + r, |r| <=
-// ln 2 / 2, ln 2 in two parts (the first of 32 bits: n times it is exact),
-// the exponential series of r to r^13 (the rest is below 2^-57).
+// ln 2 / 2, with ln 2 in two parts as Cody and Waite reduce arguments (its first
+// 32 bits, n times which is exact, and the rest rounded to 64 bits), then the
+// exponential series of r to r^13 (what follows is below 2^-57).
 __device__ inline double exp_neg(double t) {
   t = fmin(t, 750.0);                    // e^-750 < 2^-1075
   const double n = rint(t * -1.4426950408889634);
-  const double r = fma(n, -1.90821492927058770002e-10, fma(n, -6.93147180369123816490e-01, -t));
+  const double r = fma(n, -0x1.a39ef35793c76p-33, fma(n, -0x1.62e42feep-1, -t));
   double q = 1.0 / 6227020800.0;
   q = fma(q, r, 1.0 / 479001600.0);
   q = fma(q, r, 1.0 / 39916800.0);
@@ -424,7 +425,9 @@ __device__ inline int choose32(const RouteArgs &p, const IN *row, const LaneSpan
 
 // One token's choice and weights by LPT lanes: the id of rank `sub` (-1:
 // none) in lanes sub < topk, and its weight.  Scores that differ in FP32's
-// last bits decide between experts.
+// last bits decide between experts.  Softmax with a bias, or with groups by
+// their best two, has no 32-bit path: 16384 x 256, top 8, takes 33 us with a bias
+// and 24 with sigmoid scores.
 template <class IN, int LPT, int VPT>
 __device__ inline int route_token(const RouteArgs &p, const IN *row, bool live, int sub, float &weight) {
   const LaneSpan sp = lane_span(p, live, sub);
@@ -539,7 +542,10 @@ __device__ inline void route_tail(const RouteArgs &p, const RoutePlace &pl) {
 
 // Choice and weights of a block's tokens, 64 at a time, and (COUNT) the
 // block's rows of each expert; ONE: the single block of a small call places
-// its rows itself.
+// its rows itself.  Blocks of up to 1024 threads leave a lane 128 registers:
+// choose64's doubles spill 56 to 87 of them with 32 experts per lane and about
+// 12 with 16 and ONE (16384 x 1000 in 20 groups 125 us, 64 x 1000 98, 64 x 256 in 8
+// groups 18).
 template <class IN, int LPT, int VPT, bool MAPS, bool ONE>
 __global__ void route_kernel(RouteArgs p) {
   __shared__ int32_t ids[MAPS ? ROUTE_TG * MOE_MAX_TOPK : 1];
@@ -588,7 +594,10 @@ __global__ void route_kernel(RouteArgs p) {
 // counts of all blocks (its own first rows and the experts' totals), then
 // places its tokens.
 // Up to 16 waves per block: with 256 threads a block of 16384 tokens' call
-// read the 128 KB of counts in 32 dependent rounds, 9.6 us.
+// read the 128 KB of counts in 32 dependent rounds, 9.6 us.  It takes 8.1 us now;
+// beside the reads of the counts it is LDS accesses that count, half of which
+// conflict (the sums' atomics at a stride of four words, from as many row lanes
+// as a column has, and the two words of a mask).
 __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs p) {
   __shared__ int32_t ids[ROUTE_TG * MOE_MAX_TOPK];
   __shared__ RoutePlace pl;
