@@ -102,8 +102,9 @@ extern "C" int mxgemm_init(void) {
   if (hipFuncGetAttributes(&attr, (const void *)pick_dense_mx_a4(F_E4M3, MXG_NT, false, false)) != hipSuccess)
     return MXG_ERR_HIP;
   (void)cu_count();
-  const int v = int8_init();
-  return v == MXG_OK ? moe_init() : v;
+  int v = int8_init();
+  if (v == MXG_OK) v = moe_init();
+  return v == MXG_OK ? experts_init() : v;
 }
 
 extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,

@@ -179,8 +179,9 @@ __device__ inline uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
 }
 
-// Epilogue activations (after the bias, on the FP32 result).
-enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
+// Epilogue activations (after the bias, on the FP32 result).  SwiGLU takes
+// pairs of columns; activate() does not know it.
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3, ACT_SWIGLU = 8 };
 
 // Logistic function 1 / (1 + e^-y) from the hardware base-2 exponential and
 // reciprocal (each within about an ulp of FP32); saturates to 0 and 1.

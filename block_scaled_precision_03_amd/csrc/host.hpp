@@ -50,5 +50,6 @@ int int8_run(const void *A, const void *sA, const void *B, const void *sB, void 
              int64_t K, const void *bias, int act, hipStream_t stream);
 int int8_init();
 int moe_init();                          // k_moe.hip
+int experts_init();                      // k_experts.hip
 
 }  // namespace mxg

@@ -17,8 +17,6 @@
 
 namespace mxg {
 
-enum : int { ACT_SWIGLU = 8 };
-
 struct Int8Args {
   const uint8_t *A, *B;
   const float *sA, *sB;           // [M], [G, N]

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libmxgemm.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_HIP = 0, -1, -2, -3, -4
 MXFP8_E4M3, MXFP8_E5M2, MXFP4_E2M1 = 0, 1, 4
 FP8_E4M3_TENSOR, FP8_E5M2_TENSOR = 16, 17
+FP8_E4M3_BLOCK = 18
 INT8 = 32
 BF16, F32 = 64, 65
 PRESHUFFLED = 0x100
@@ -40,6 +41,7 @@ EXPORTS = (
     "mxgemm_quantize_mx", "mxgemm_quantize_tensor", "grouped_fp8_quantize_act", "grouped_fp8_quantize_weight",
     "grouped_int8_gemm_run", "grouped_int8_gemm_validate", "grouped_int8_gemm_variant", "mxgemm_quantize_int8",
     "moe_route_workspace_bytes", "moe_route", "moe_route_backward", "moe_combine", "moe_combine_backward",
+    "moe_experts_workspace_bytes", "moe_experts", "moe_experts_validate",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -125,6 +127,12 @@ _lib.moe_combine.restype = _i
 _lib.moe_combine.argtypes = [_p, _p, _p, _p, _i64, _i, _i64, _i64, _p]
 _lib.moe_combine_backward.restype = _i
 _lib.moe_combine_backward.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i, _i64, _i64, _p]
+_lib.moe_experts_workspace_bytes.restype = _i64
+_lib.moe_experts_workspace_bytes.argtypes = [_i64, _i, _i64]
+_lib.moe_experts.restype = _i
+_lib.moe_experts.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i64, _i64, _i, _p, _i64, _p]
+_lib.moe_experts_validate.restype = _i
+_lib.moe_experts_validate.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i64, _i64, _i, _p, _i64]
 
 
 class MxgemmError(RuntimeError):
@@ -172,6 +180,18 @@ def _stream(stream):
             _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream
         return handle
     return _current_raw_stream()
+
+
+def _workspace(workspace, needed):
+    """Address and bytes of a workspace: a device tensor, or an address of
+    `needed()` bytes."""
+    if workspace is None:
+        nbytes = 0
+    elif isinstance(workspace, int):
+        nbytes = needed()
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    return (_ptr(workspace) if nbytes > 0 else None), nbytes
 
 
 def _check(rc, what):
@@ -371,13 +391,7 @@ def moe_route(dtype, logits, bias, ids, weights, T, E, topk, score=MOE_SOFTMAX, 
     m_sizes, row_of and slot_of, the order of the experts' rows; workspace:
     a device tensor of moe_route_workspace_bytes(T, E) bytes or more (see
     include/mxgemm.h)."""
-    if workspace is None:
-        nbytes = 0
-    elif isinstance(workspace, int):
-        nbytes = _lib.moe_route_workspace_bytes(T, E)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    ws = _ptr(workspace) if nbytes > 0 else None
+    ws, nbytes = _workspace(workspace, lambda: _lib.moe_route_workspace_bytes(T, E))
     _check(_lib.moe_route(dtype, _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), T, E, topk, score, n_group,
                           topk_group, group_score, int(bool(renormalize)), scale, _ptr(m_sizes), _ptr(row_of),
                           _ptr(slot_of), ws, nbytes, _stream(stream)), "moe_route")
@@ -401,3 +415,26 @@ def moe_combine_backward(dout, y, w, row_of, dy, dw, T, topk, N, rows, stream=No
     """Gradient of moe_combine: dy (the rows that row_of names) and dw [T, topk]."""
     _check(_lib.moe_combine_backward(_ptr(dout), _ptr(y), _ptr(w), _ptr(row_of), _ptr(dy), _ptr(dw), T, topk, N,
                                      rows, _stream(stream)), "moe_combine_backward")
+
+
+def moe_experts_workspace_bytes(T, topk, F):
+    return _lib.moe_experts_workspace_bytes(T, topk, F)
+
+
+def moe_experts(fmt, x, ids, weights, w1, s1, w2, s2, out, T, E, topk, D, F, activation=ACT_SWIGLU, residual=None,
+                workspace=None, stream=None):
+    """out[t] = residual[t] + sum of the chosen experts' weighted results, for
+    T <= 64 tokens (see include/mxgemm.h); fmt: INT8, BF16, MXFP8_E4M3,
+    MXFP8_E5M2, MXFP4_E2M1 or FP8_E4M3_BLOCK; workspace: a device tensor of
+    moe_experts_workspace_bytes(T, topk, F) bytes or more."""
+    ws, nbytes = _workspace(workspace, lambda: _lib.moe_experts_workspace_bytes(T, topk, F))
+    _check(_lib.moe_experts(fmt, _ptr(x), _ptr(ids), _ptr(weights), _ptr(w1), _ptr(s1), _ptr(w2), _ptr(s2),
+                            _ptr(residual), _ptr(out), T, E, topk, D, F, activation, ws, nbytes, _stream(stream)),
+           "moe_experts")
+
+
+def moe_experts_validate(fmt, x, ids, weights, w1, s1, w2, s2, out, T, E, topk, D, F, activation=ACT_SWIGLU,
+                         residual=None, workspace=None):
+    ws, nbytes = _workspace(workspace, lambda: _lib.moe_experts_workspace_bytes(T, topk, F))
+    return _lib.moe_experts_validate(fmt, _ptr(x), _ptr(ids), _ptr(weights), _ptr(w1), _ptr(s1), _ptr(w2), _ptr(s2),
+                                     _ptr(residual), _ptr(out), T, E, topk, D, F, activation, ws, nbytes)

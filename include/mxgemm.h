@@ -27,12 +27,12 @@
  * Conventions for every entry point:
  *  - All data pointers are DEVICE pointers owned by the caller.  The library
  *    never allocates, frees or retains caller memory and uses no workspace
- *    (moe_route alone takes one from the caller; see there).
+ *    (moe_route and moe_experts take one from the caller; see there).
  *  - Calls are stream-ordered and asynchronous: exactly one kernel is
  *    enqueued on `stream` (0 = the null stream) per successful call, with
- *    two exceptions: mxgemm_quantize_tensor enqueues four (its scale output
+ *    these exceptions: mxgemm_quantize_tensor enqueues four (its scale output
  *    serves as the amax word between them; see there), moe_route at most
- *    two (see there), and
+ *    two (see there), moe_experts two, and
  *    grouped_fp8_gemm_run and grouped_bf16_gemm_run enqueue two when they
  *    run MXG_GROUPED_TILED on more 256 x 256 tiles than the device has
  *    compute units (see grouped_fp8_gemm_variant).  The tuning call grouped_fp8_gemm_autotune
@@ -667,6 +667,57 @@ int moe_combine(const void *y, const float *w, const int32_t *row_of, void *out,
                 int64_t N, int64_t rows, hipStream_t stream);
 int moe_combine_backward(const void *dout, const void *y, const float *w, const int32_t *row_of, void *dy,
                          float *dw, int64_t T, int topk, int64_t N, int64_t rows, hipStream_t stream);
+
+/* A weight format of moe_experts alone: the weights of grouped_fp8_gemm_run
+ * (E4M3 codes [N,K], one FP32 scale per 128 x 128 block, [N/128, K/128]). */
+enum { MXG_FP8_E4M3_BLOCK = 18 };
+
+/*
+ * moe_experts -- the experts of a mixture-of-experts layer for a few tokens,
+ * from moe_route's choice to the layer's result, in two kernels:
+ *
+ *   out[t] = residual[t] + sum_e share[t,e] W2[e] act( W1[e] x[t] ),
+ *   share[t,e] = the sum of weights[t,j] over the slots j with ids[t,j] = e.
+ *
+ * A decode step's form of quantize, grouped product, quantize, grouped
+ * product, combine: the chosen experts' weights are read once, in any of
+ * these formats, and the activations are not quantized.
+ *
+ * fmt     the weights' format, both [N,K] row-major for every expert:
+ *         MXG_INT8 (scales FP32 [E,N]), MXG_BF16 (no scales, NULL),
+ *         MXG_MXFP8_E4M3, MXG_MXFP8_E5M2, MXG_MXFP4_E2M1 (E8M0 [E,N,K/32]),
+ *         MXG_FP8_E4M3_BLOCK (FP32 [E,N/128,K/128]).
+ * x       BF16 [T, D]; ids int32 and weights FP32 [T, topk], as moe_route
+ *         writes them (no row maps are needed): ids outside [0, E) are skipped,
+ *         an expert named twice by a token counts with both weights.
+ * w1, s1  [E, F, D], with MXG_ACT_SWIGLU [E, 2F, D] with row 2j the gate's
+ *         channel j and row 2j + 1 the up's (as grouped_int8_gemm_run).
+ * w2, s2  [E, D, F].
+ * residual  BF16 [T, D] or NULL; out BF16 [T, D].  out may be the same buffer
+ *         as residual or x; a token without experts gets its residual (or 0).
+ * activation  MXG_ACT_*, on the FP32 sums; its result is held to 16 bits of
+ *         mantissa for the second product, whose sums are FP32, and out is
+ *         rounded once.  MX values beyond BF16's range are rounded to it.
+ * workspace, workspace_bytes  16-byte aligned device memory of at least
+ *         moe_experts_workspace_bytes(T, topk, F) bytes, free for other use once
+ *         the call's work is done; calls that may run at the same time need one
+ *         each.
+ * T <= 64 (more: the grouped products), E <= 1024, topk <= 32, D and F <= 131072,
+ * both multiples of 16 (INT8), 8 (BF16), 32 (MX) or 128 (block): else
+ * MXG_ERR_UNSUPPORTED; an unknown enum, null pointer, negative size, E or topk
+ * below 1 or a small workspace is MXG_ERR_INVALID_ARG; x, weights, residual, out
+ * and workspace 16-byte aligned, FP32 and int32 arrays 4-byte.  T or D = 0:
+ * no-op; F = 0: out = residual (or 0).  The sums' order is fixed: the same call
+ * gives the same bits.  Device ids are never read by the host.
+ */
+int64_t moe_experts_workspace_bytes(int64_t T, int topk, int64_t F);
+int moe_experts(int fmt, const void *x, const int32_t *ids, const float *weights, const void *w1, const void *s1,
+                const void *w2, const void *s2, const void *residual, void *out, int64_t T, int64_t E, int topk,
+                int64_t D, int64_t F, int activation, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float *weights, const void *w1,
+                         const void *s1, const void *w2, const void *s2, const void *residual, const void *out,
+                         int64_t T, int64_t E, int topk, int64_t D, int64_t F, int activation, const void *workspace,
+                         int64_t workspace_bytes);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,98 @@
+"""CPU checks of the few-token experts' entry points (host checks only, nothing
+reaches a device) and of their 64-bit reference's formats."""
+import numpy as np
+import pytest
+
+import oracle
+from tests import experts_ref as R
+
+P = 1 << 20       # a fake, aligned address (never dereferenced)
+
+
+def _mx():
+    from block_scaled_precision_03_amd import mxgemm
+    return mxgemm
+
+
+def ok(**kw):
+    a = dict(fmt=R.INT8, x=P, ids=P, weights=P, w1=P, s1=P, w2=P, s2=P, out=P, T=3, E=8, topk=2, D=64, F=32, activation=8,
+             residual=P, workspace=P)
+    a.update(kw)
+    return _mx().moe_experts_validate(**a)
+
+
+GOOD = [dict(), dict(residual=None), dict(T=64), dict(E=1024), dict(topk=32), dict(E=1, topk=2), dict(activation=0),
+        dict(activation=3), dict(ids=P + 4), dict(weights=P + 4), dict(s1=P + 4), dict(T=0, x=0, ids=0, out=0, workspace=None),
+        dict(D=0, out=0), dict(F=0, w1=0, w2=0, x=0), dict(fmt=R.BF16, s1=0, s2=0, D=8, F=8), dict(fmt=R.E4M3, s1=P + 1, s2=P + 3),
+        dict(fmt=R.E5M2), dict(fmt=R.E2M1, D=32, F=96), dict(fmt=R.BLOCK, D=128, F=256), dict(D=131072, F=131072)]
+BAD = [(dict(fmt=16), -1), (dict(fmt=65), -1), (dict(fmt=2), -1), (dict(fmt=R.E4M3 | 0x100), -1),
+       (dict(activation=4), -1), (dict(activation=-1), -1), (dict(activation=9), -1),
+       (dict(T=-1), -1), (dict(E=0), -1), (dict(topk=0), -1), (dict(D=-16), -1), (dict(F=-16), -1),
+       (dict(T=65), -2), (dict(E=1025), -2), (dict(topk=33), -2), (dict(D=131088), -2), (dict(F=131088), -2),
+       (dict(D=72), -2), (dict(F=40), -2), (dict(fmt=R.BF16, D=12), -2), (dict(fmt=R.E4M3, D=48), -2),
+       (dict(fmt=R.E2M1, F=16), -2), (dict(fmt=R.BLOCK, D=128, F=64), -2),
+       (dict(x=0), -1), (dict(ids=0), -1), (dict(weights=0), -1), (dict(w1=0), -1), (dict(s1=0), -1), (dict(w2=0), -1),
+       (dict(s2=0), -1), (dict(out=0), -1), (dict(workspace=None), -1), (dict(fmt=R.E4M3, s2=0), -1),
+       (dict(x=P + 8), -3), (dict(out=P + 2), -3), (dict(residual=P + 2), -3), (dict(w1=P + 8), -3), (dict(w2=P + 4), -3),
+       (dict(ids=P + 2), -3), (dict(weights=P + 1), -3), (dict(s1=P + 2), -3), (dict(workspace=P + 8), -3)]
+
+
+@pytest.mark.parametrize("kw", GOOD)
+def test_accepts(kw):
+    assert ok(**kw) == 0
+
+
+@pytest.mark.parametrize("kw,status", BAD)
+def test_refuses(kw, status):
+    assert ok(**kw) == status
+    # the call itself refuses the same before anything reaches a device
+    m = _mx()
+    a = dict(fmt=R.INT8, x=P, ids=P, weights=P, w1=P, s1=P, w2=P, s2=P, out=P, T=3, E=8, topk=2, D=64, F=32, activation=8,
+             residual=P, workspace=P, stream=0)
+    a.update(kw)
+    with pytest.raises(m.MxgemmError) as err:
+        m.moe_experts(**a)
+    assert err.value.status == status
+
+
+def test_workspace():
+    m = _mx()
+    assert m.moe_experts_workspace_bytes(1, 4, 512) >= 4 * 4 * 512
+    assert m.moe_experts_workspace_bytes(0, 1, 0) >= 0
+    for bad in ((-1, 4, 16), (65, 4, 16), (1, 0, 16), (1, 33, 16), (1, 4, -1), (1, 4, 131073)):
+        assert m.moe_experts_workspace_bytes(*bad) == -1
+    import torch
+    need = m.moe_experts_workspace_bytes(3, 2, 32)
+    room = torch.empty(need + 32, dtype=torch.uint8)
+    start = -room.data_ptr() % 16
+    assert ok(workspace=room[start:start + need]) == 0
+    assert ok(workspace=room[start:start + need - 1]) == -1
+
+
+def test_formats_agree_with_the_oracle():
+    c = np.arange(256, dtype=np.uint8)
+    for fmt, e, m, bias, nan in ((oracle.E4M3, 4, 3, 7, 127), (oracle.E5M2, 5, 2, 15, 124)):
+        real = (c & nan) != nan
+        assert (R._small_float(c.astype(np.int64), e, m, bias) == oracle.decode(fmt, c))[real].all()
+    assert (R._small_float(np.arange(16), 2, 1, 1) == oracle.decode(oracle.E2M1, np.arange(16, dtype=np.uint8))).all()
+
+
+@pytest.mark.parametrize("name", sorted(R.FORMATS))
+def test_reference_is_the_formula(name):
+    """Against one written out term by term."""
+    fmt, rng = R.FORMATS[name], np.random.default_rng(0)
+    u = R.UNIT[fmt]
+    E, F, D = 3, u, u
+    (_, _, v1), (_, _, v2) = R.encode(rng, fmt, E, 2 * F, D, 0.3), R.encode(rng, fmt, E, D, F, 0.3)
+    x, r = rng.standard_normal((2, D)).astype(np.float32), rng.standard_normal((2, D)).astype(np.float32)
+    ids, w = np.array([[2, 0, 2], [-1, 1, 9]]), rng.random((2, 3)).astype(np.float32)
+    out, tol = R.experts(x, ids, w, v1, v2, R.ACT_SWIGLU, r)
+    for t in range(2):
+        for d in range(0, D, 7):
+            s = float(r[t, d])
+            for j in range(3):
+                if 0 <= ids[t, j] < E:
+                    z = [sum(float(v1[ids[t, j], n, k]) * float(x[t, k]) for k in range(D)) for n in range(2 * F)]
+                    h = [z[2 * f] / (1 + np.exp(-z[2 * f])) * z[2 * f + 1] for f in range(F)]
+                    s += float(w[t, j]) * sum(float(v2[ids[t, j], d, f]) * h[f] for f in range(F))
+            assert abs(out[t, d] - s) <= 1e-9 * max(1.0, abs(s)) and tol[t, d] > 0
