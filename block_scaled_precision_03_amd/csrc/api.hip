@@ -104,7 +104,8 @@ extern "C" int mxgemm_init(void) {
   (void)cu_count();
   int v = int8_init();
   if (v == MXG_OK) v = moe_init();
-  return v == MXG_OK ? experts_init() : v;
+  if (v == MXG_OK) v = experts_init();
+  return v == MXG_OK ? residual_init() : v;
 }
 
 extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,
@@ -153,7 +154,7 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
 namespace {
 // Kernel selection for the dense path (the instantiations live in the k_*.hip
 // translation units).
-dense_fn pick_dense(int ea, int eb, bool mx, int layout, bool psb, bool fuse) {
+dense_fn pick_dense(int ea, int eb, bool mx, int layout, bool psb, int fuse) {
   if (ea == F_E2M1 || eb == F_E2M1)
     return (ea == F_E2M1 && eb == F_E2M1 && mx) ? pick_dense_fp4(layout, psb, fuse) : nullptr;
   if (ea == F_E4M3) return mx ? pick_dense_mx_a4(eb, layout, psb, fuse) : pick_dense_tw_a4(eb, layout, psb, fuse);
@@ -166,24 +167,30 @@ __global__ void zero_bf16_kernel(uint16_t *D, int64_t n) {
   if (i < n) D[i] = 0;
 }
 
-// K == 0 with the fused epilogue: D[m, n] = act(0 + bias[n]).
-__global__ void bias_act_fill_kernel(uint16_t *D, int64_t M, int64_t N, const uint16_t *bias, int act) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// K == 0 with the fused epilogue: D[m, n] = act(0 + bias[n]) + R[m, n].
+__global__ void bias_act_fill_kernel(uint16_t *D, int64_t M, int64_t N, const uint16_t *bias, int act,
+                                     const uint16_t *R, uint16_t *Z) {
+  const int64_t i = flat_block() * 256 + threadIdx.x;
   if (i >= M * N) return;
   const float z = bias ? __uint_as_float((uint32_t)bias[i % N] << 16) : 0.0f;
-  D[i] = (uint16_t)pack_bf16x2(activate(act, z), 0.0f);
+  float v = activate(act, z);
+  if (R) v += __uint_as_float((uint32_t)R[i] << 16);
+  if (Z) Z[i] = (uint16_t)pack_bf16x2(z, 0.0f);
+  D[i] = (uint16_t)pack_bf16x2(v, 0.0f);
 }
 
 int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
-              void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, hipStream_t stream) {
-  if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, stream);
-  const bool fuse = bias != nullptr || act != MXG_ACT_NONE;
+              void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, const void *residual, void *z,
+              hipStream_t stream) {
+  if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, residual, z, stream);
+  const int fuse = residual != nullptr || z != nullptr ? FUSE_RES
+                   : bias != nullptr || act != MXG_ACT_NONE ? FUSE_ACT : FUSE_NONE;
   if (M == 0 || N == 0) return MXG_OK;
   if (K == 0) {
     const int64_t n = M * N;
-    if (fuse)
-      hipLaunchKernelGGL(bias_act_fill_kernel, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, stream,
-                         (uint16_t *)D, M, N, (const uint16_t *)bias, act);
+    if (fuse != FUSE_NONE)
+      hipLaunchKernelGGL(bias_act_fill_kernel, flat_grid(cdiv(n, 256)), dim3(256), 0, stream, (uint16_t *)D, M, N,
+                         (const uint16_t *)bias, act, (const uint16_t *)residual, (uint16_t *)z);
     else
       hipLaunchKernelGGL(zero_bf16_kernel, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, stream,
                          (uint16_t *)D, n);
@@ -212,6 +219,8 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   a.tiles_n = (int)cdiv(N, small ? SBN : DBN);
   a.bias = (const uint16_t *)bias;
   a.act = act;
+  a.R = (const uint16_t *)residual;
+  a.Z = (uint16_t *)z;
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   if (tiles > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
   if (small) {
@@ -230,7 +239,7 @@ extern "C" int mxgemm_run(int fmtA, int fmtB, int layout, const void *A, const v
                const void *sB, void *D, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int v = mxgemm_validate(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K);
   if (v != MXG_OK) return v;
-  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, nullptr, MXG_ACT_NONE, stream);
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, nullptr, MXG_ACT_NONE, nullptr, nullptr, stream);
 }
 
 extern "C" int mxgemm_validate_fused(int fmtA, int fmtB, int layout, const void *A, const void *sA,
@@ -257,7 +266,28 @@ extern "C" int mxgemm_run_fused(int fmtA, int fmtB, int layout, const void *A, c
                                 int activation, hipStream_t stream) {
   const int v = mxgemm_validate_fused(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation);
   if (v != MXG_OK) return v;
-  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, stream);
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, nullptr, nullptr, stream);
+}
+
+extern "C" int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B,
+                                        const void *sB, const void *D, int64_t M, int64_t N, int64_t K, const void *bias,
+                                        int activation, const void *residual, const void *z) {
+  const int v = mxgemm_validate_fused(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation);
+  if (v != MXG_OK) return v;
+  if (residual == nullptr && z == nullptr) return MXG_OK;
+  if (layout != MXG_NT) return MXG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MXG_OK;
+  if (z != nullptr && (z == D || z == residual)) return MXG_ERR_INVALID_ARG;
+  if (!aligned(residual, 16) || !aligned(z, 16)) return MXG_ERR_MISALIGNED;
+  return MXG_OK;
+}
+
+extern "C" int mxgemm_run_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B,
+                                   const void *sB, void *D, int64_t M, int64_t N, int64_t K, const void *bias,
+                                   int activation, const void *residual, void *z, hipStream_t stream) {
+  const int v = mxgemm_validate_residual(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, residual, z);
+  if (v != MXG_OK) return v;
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, residual, z, stream);
 }
 
 extern "C" int grouped_fp8_gemm_validate(int G, const int64_t *m_sizes, const void *XQ, const float *x_scale,

@@ -46,7 +46,14 @@ struct DenseArgs {
   int tail_grid, tail_rounds;     // groupwise only: see grouped_split_end
   const uint16_t *bias;           // fused epilogue: BF16 [N] or null
   int act;                        // fused epilogue: ACT_*
+  const uint16_t *R;              // residual epilogue: BF16 [M, N] added after the activation, or null
+  uint16_t *Z;                    // residual epilogue: the activation's argument in BF16 [M, N], or null
 };
+
+// What a dense kernel does to a finished sum before its rounding to BF16:
+// nothing; bias and activation; bias, activation, residual (and the
+// activation's argument stored beside the result).
+enum : int { FUSE_NONE = 0, FUSE_ACT = 1, FUSE_RES = 2 };
 
 // One output tile: origin, the row limit of its stores (M, or the end of its
 // group) and, for the grouped GEMM, its group (index, first row, rows).
@@ -119,8 +126,9 @@ __device__ inline void wait_vmem_le() {
 // from registers while that stage streams in, so no compute unit idles on an
 // epilogue, a workgroup launch or a cold first stage between tiles.
 //
-template <int FA, int FB, int SMODE, bool TA, bool TB, bool PSB, bool FUSE = false>
+template <int FA, int FB, int SMODE, bool TA, bool TB, bool PSB, int FUSE = FUSE_NONE>
 struct DenseLoop {
+  static constexpr bool RES = FUSE == FUSE_RES;
   static constexpr bool FP4 = (FA == F_E2M1);
   static constexpr bool MX = (SMODE == SM_MX);
   static constexpr bool GROUP = (SMODE == SM_GROUP);
@@ -582,7 +590,27 @@ struct DenseLoop {
     e.voff = (uint32_t)(2 * ((c.wm * (FM * 16) + i) * p.N + c.wn * (FN * 16) + 16 * (q & 1) + 8 * (q >> 1)));
   }
 
-  __device__ static inline void store_rows(const Ctx &c, const Epi &e, int a, const v4f (&row_in)[FN]) {
+  // The residual beside row tile a of a full tile: lane (i, q) holds row 16 a
+  // + i, columns 16 b + 4 q .. + 3 of the wave's block, as its sums do.  The
+  // offsets are those of the stores (see make_epi), so the same sizes bound
+  // them.  Without a residual the resource is empty: zeros, no memory read.
+  typedef v2i ResRow[RES ? FN : 1];
+  __device__ static inline void load_residual(const Ctx &c, const Epi &e, int a, ResRow &r) {
+    if constexpr (RES) {
+      const DenseArgs &p = *c.p;
+      const int64_t org = (int64_t)e.m0 * p.N + e.n0;
+      const __amdgpu_buffer_rsrc_t rr =
+          p.R ? make_rsrc(p.R + org, clamp_records(2 * (p.M * p.N - org))) : make_rsrc(p.D, 0);
+      const int lane = (int)__lane_id(), i = lane & 15, q = lane >> 4;
+      const uint32_t o = (uint32_t)(2 * ((c.wm * (FM * 16) + a * 16 + i) * p.N + c.wn * (FN * 16) + 4 * q));
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+        r[b] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rr, (int)(o + 32u * b), 0, 0));
+    }
+  }
+
+  __device__ static inline void store_rows(const Ctx &c, const Epi &e, int a, const v4f (&row_in)[FN],
+                                           const ResRow &res) {
     const float al = e.alpha;
     // alpha is 1 unless the operands are tensor-wise: no multiply
     v4f row[FN];
@@ -600,6 +628,12 @@ struct DenseLoop {
         v.y += __uint_as_float((uint32_t)w.x & 0xFFFF0000u);
         v.z += __uint_as_float((uint32_t)w.y << 16);
         v.w += __uint_as_float((uint32_t)w.y & 0xFFFF0000u);
+      }
+      return v;
+    };
+    // The activation (and the residual) after it.
+    auto activated = [&](v4f v, const v2i &r) -> v4f {
+      if constexpr (FUSE) {
         const int act = e.act;
         if (act != ACT_NONE) {
           v.x = activate(act, v.x);
@@ -607,6 +641,12 @@ struct DenseLoop {
           v.z = activate(act, v.z);
           v.w = activate(act, v.w);
         }
+      }
+      if constexpr (RES) {
+        v.x += __uint_as_float((uint32_t)r.x << 16);
+        v.y += __uint_as_float((uint32_t)r.x & 0xFFFF0000u);
+        v.z += __uint_as_float((uint32_t)r.y << 16);
+        v.w += __uint_as_float((uint32_t)r.y & 0xFFFF0000u);
       }
       return v;
     };
@@ -617,9 +657,7 @@ struct DenseLoop {
       const int lane = (int)__lane_id();
       const bool odd = ((lane >> 4) & 1) != 0;
       const int partner = (lane ^ 16) << 2;
-#pragma unroll
-      for (int pr = 0; pr < FN / 2; ++pr) {
-        const v4f x = finish(row[2 * pr], 2 * pr), y = finish(row[2 * pr + 1], 2 * pr + 1);
+      auto put = [&](const v4f &x, const v4f &y, const u32x4 &rd, int pr) {
         const uint32_t xlo = pack_bf16x2(x.x, x.y), xhi = pack_bf16x2(x.z, x.w);
         const uint32_t ylo = pack_bf16x2(y.x, y.y), yhi = pack_bf16x2(y.z, y.w);
         // q even keeps its tile-2p chunk and takes the partner's; q odd the
@@ -628,7 +666,21 @@ struct DenseLoop {
         const uint32_t rhi = (uint32_t)__builtin_amdgcn_ds_bpermute(partner, (int)(odd ? xhi : yhi));
         const v4i v = odd ? (v4i){(int)rlo, (int)rhi, (int)ylo, (int)yhi}
                           : (v4i){(int)xlo, (int)xhi, (int)rlo, (int)rhi};
-        store16_asm(v, e.rd, e.voff, (uint32_t)a * rs + 64u * pr);
+        store16_asm(v, rd, e.voff, (uint32_t)a * rs + 64u * pr);
+      };
+#pragma unroll
+      for (int pr = 0; pr < FN / 2; ++pr) {
+        const v4f x = finish(row[2 * pr], 2 * pr), y = finish(row[2 * pr + 1], 2 * pr + 1);
+        if constexpr (RES) {
+          const DenseArgs &p = *c.p;
+          if (p.Z) {
+            const int64_t org = (int64_t)e.m0 * p.N + e.n0;
+            put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))), pr);
+          }
+          put(activated(x, res[2 * pr]), activated(y, res[2 * pr + 1]), e.rd, pr);
+        } else {
+          put(activated(x, v2i{}), activated(y, v2i{}), e.rd, pr);
+        }
       }
     } else {
       // edge tiles: lane position recomputed here rather than kept live
@@ -639,9 +691,26 @@ struct DenseLoop {
         uint16_t *dst = p.D + r * p.N;
 #pragma unroll
         for (int b = 0; b < FN; ++b) {
-          const v4f v = finish(row[b], b);
-          const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+          const v4f z = finish(row[b], b);
           const int64_t col = (int64_t)e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q;
+          v2i near = {0, 0};
+          if constexpr (RES) {
+            if (p.R) {
+              uint16_t h[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (col + k < p.N) h[k] = p.R[r * p.N + col + k];
+              near = (v2i){(int)(h[0] | (uint32_t)h[1] << 16), (int)(h[2] | (uint32_t)h[3] << 16)};
+            }
+            if (p.Z) {
+              const uint32_t uz[2] = {pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w)};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (col + k < p.N) p.Z[r * p.N + col + k] = (uint16_t)(uz[k >> 1] >> (16 * (k & 1)));
+            }
+          }
+          const v4f v = activated(z, near);
+          const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (col + k < p.N) dst[col + k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
@@ -697,6 +766,12 @@ struct DenseLoop {
       }
       return E8M0_ONE_X4;
     };
+    // The residual of a row tile is loaded while the row tile before it is
+    // finished.
+    ResRow res[2];
+    if constexpr (EPI && RES) {
+      if (e.on && e.full) load_residual(c, e, 0, res[0]);
+    }
     // A stage of two K steps (FP4) reads both steps' B fragments and scales
     // up front, so that the second step's reads overlap the first step's
     // matrix work instead of stalling between the two (not in the first step
@@ -774,7 +849,7 @@ struct DenseLoop {
             scp[a & 1] = __uint_as_float(saw[a]) * wsv;
             // the previous tile's rows leave before this tile's partials
             // replace them (one row tile later)
-            if (EPI && s == 0 && e.on) store_rows(c, e, a, acc[a]);
+            if (EPI && s == 0 && e.on) store_rows(c, e, a, acc[a], res[0]);
 #pragma unroll
             for (int b = 0; b < FN; ++b)
               part[a & 1][b] = mfma_scaled<FB, FA>(bf[b], af, zero, E8M0_ONE_X4, E8M0_ONE_X4);
@@ -827,7 +902,12 @@ struct DenseLoop {
         int sa = E8M0_ONE_X4;
         if constexpr (MX) sa = (int)((SA_AHEAD ? saw[0] : saw[a]) >> (8 * c.q));
         if (EPI && s == 0) {
-          if (e.on) store_rows(c, e, a, acc[a]);
+          if (e.on) {
+            if constexpr (RES) {
+              if (e.full && a + 1 < FM) load_residual(c, e, a + 1, res[(a + 1) & 1]);
+            }
+            store_rows(c, e, a, acc[a], res[a & 1]);
+          }
 #pragma unroll
           for (int b = 0; b < FN; ++b) {
             if constexpr (BF) acc[a][b] = mfma_bf16_x2(bf[b], af, (v4f){0.f, 0.f, 0.f, 0.f});
@@ -955,8 +1035,15 @@ struct DenseLoop {
         }
       }
     }
+    ResRow res[FM];
+    if constexpr (RES) {
+      if (e.full) {
 #pragma unroll
-    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a]);
+        for (int a = 0; a < FM; ++a) load_residual(c, e, a, res[a]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a], res[a]);
   }
 };
 
@@ -987,7 +1074,7 @@ __device__ inline void persistent_tile(int bid, int k, int P, int tiles_m, int t
   tile_in_order(b, tiles_m, tiles_n, tm, tn);
 }
 
-template <int FA, int FB, int SMODE, bool TA, bool TB, bool PSB, bool FUSE = false>
+template <int FA, int FB, int SMODE, bool TA, bool TB, bool PSB, int FUSE = FUSE_NONE>
 __global__ __launch_bounds__(DNW8 * 64, 1) void dense_kernel(DenseArgs p) {
   typedef DenseLoop<FA, FB, SMODE, TA, TB, PSB, FUSE> L;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::LDS_BYTES];

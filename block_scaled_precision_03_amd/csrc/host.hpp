@@ -47,9 +47,10 @@ int int8_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,
                   const void *D, int64_t M, int64_t N, int64_t K);
 int int8_dense_variant(int64_t M, int64_t N, int64_t K);
 int int8_run(const void *A, const void *sA, const void *B, const void *sB, void *D, int64_t M, int64_t N,
-             int64_t K, const void *bias, int act, hipStream_t stream);
+             int64_t K, const void *bias, int act, const void *residual, void *z, hipStream_t stream);
 int int8_init();
 int moe_init();                          // k_moe.hip
 int experts_init();                      // k_experts.hip
+int residual_init();                     // k_residual.hip
 
 }  // namespace mxg

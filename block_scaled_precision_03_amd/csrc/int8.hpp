@@ -25,6 +25,8 @@ struct Int8Args {
   uint16_t *D;                    // [M, No], No = N or (SwiGLU) N / 2
   int64_t M, N, K, No;
   int G, act, tiles_n;
+  const uint16_t *R;              // RES kernels: BF16 [M, No] added after the activation, or null
+  uint16_t *Z;                    // RES kernels: the activation's argument in BF16 [M, N], or null
 };
 
 // D += the 16x16x64 block of signed bytes: lane (i = lane % 16, q = lane / 16)
@@ -93,6 +95,63 @@ __device__ inline void int8_store4(const Int8Args &p, int act, int64_t row, int6
   }
 }
 
+// N values of a BF16 row of which `room` are left, at any alignment.
+template <int N>
+__device__ inline void load_bf16_any(const uint16_t *src, int64_t room, float (&v)[N]) {
+  uint16_t h[N];
+  if (room >= N) {
+    __builtin_memcpy(h, src, 2 * N);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) h[k] = k < room ? src[k] : (uint16_t)0;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __uint_as_float((uint32_t)h[k] << 16);
+}
+template <int N>
+__device__ inline void store_bf16_any(uint16_t *dst, int64_t room, const float (&v)[N]) {
+  uint32_t u[N / 2];
+#pragma unroll
+  for (int k = 0; k < N / 2; ++k) u[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+  if (room >= N) {
+    __builtin_memcpy(dst, u, 2 * N);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < room) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
+  }
+}
+
+// Four consecutive columns of the product, scaled and biased but not
+// activated, to what the call returns; RES: the activation's argument too,
+// and the residual added.
+template <bool RES>
+__device__ inline void int8_emit4(const Int8Args &p, int act, int64_t row, int64_t col, v4f z) {
+  if constexpr (!RES) {
+    if (act != ACT_NONE && act != ACT_SWIGLU) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[k] = activate(act, z[k]);
+    }
+    int8_store4(p, act, row, col, z);
+  } else {
+    if (p.Z) store_bf16_any<4>(p.Z + row * p.N + col, p.N - col, {z.x, z.y, z.z, z.w});
+    if (act == ACT_SWIGLU) {
+      const int64_t oc = col >> 1;
+      float r[2] = {0.f, 0.f};
+      if (p.R) load_bf16_any<2>(p.R + row * p.No + oc, p.No - oc, r);
+      const float v[2] = {z.x * logistic_f32(z.x) * z.y + r[0], z.z * logistic_f32(z.z) * z.w + r[1]};
+      store_bf16_any<2>(p.D + row * p.No + oc, p.No - oc, v);
+    } else {
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+      if (p.R) load_bf16_any<4>(p.R + row * p.No + col, p.No - col, r);
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = activate(act, z[k]) + r[k];
+      store_bf16_any<4>(p.D + row * p.No + col, p.No - col, v);
+    }
+  }
+}
+
 // The FP32 channel scales and biases of the four consecutive columns n0 + c
 // .. from memory (n0 uniform; columns past N read 0, their results are never
 // stored), by range-checked loads: with a branch per column their latencies
@@ -123,7 +182,7 @@ __device__ inline void int8_columns(const Int8Args &p, int g, int64_t n0, int c,
 // The activation is a template argument: as a switch on a kernel argument,
 // repeated for each of the tile's 128 accumulators, it made 34 K instructions
 // with 216 scratch accesses (5.1 ms for M = 16384, N = 14336, K = 4096).
-template <int ACT>
+template <int ACT, bool RES>
 struct Int8Loop {
   static constexpr bool SWIGLU = ACT == ACT_SWIGLU;
   static constexpr int FM = 8, FN = 4;
@@ -221,7 +280,7 @@ struct Int8Loop {
     e.on = on;
     // 16-byte stores through a range-checked 32-bit offset (see DenseLoop), at
     // any alignment
-    e.full = t.m0 + DBM <= t.lim && t.n0 + DBN <= p.N && p.No <= (1 << 22);
+    e.full = t.m0 + DBM <= t.lim && t.n0 + DBN <= p.N && (RES ? p.N : p.No) <= (1 << 22);
     const int64_t org = t.m0 * p.No + (SWIGLU ? t.n0 / 2 : t.n0);
     e.rd = rsrc4(p.D + org, clamp_records(2 * (p.M * p.No - org)));
     e.rowstride = (uint32_t)(32 * p.No);
@@ -231,12 +290,34 @@ struct Int8Loop {
     else e.voff = (uint32_t)(2 * (r * p.No + c.wn * 64 + 16 * (q & 1) + 8 * (q >> 1)));
   }
 
+  // The residual beside row tile a of a full tile, as its sums lie: four
+  // columns per lane and 16-column block, SwiGLU two.  The offsets are those
+  // of the stores, so the same sizes bound them.
+  typedef v2i ResRow[RES ? FN : 1];
+  __device__ static inline void load_residual(const Ctx &c, const Epi &e, int a, ResRow &r) {
+    if constexpr (RES) {
+      const Int8Args &p = *c.p;
+      const int64_t org = e.m0 * p.No + (SWIGLU ? e.n0 / 2 : e.n0);
+      const __amdgpu_buffer_rsrc_t rr =
+          p.R ? make_rsrc(p.R + org, clamp_records(2 * (p.M * p.No - org))) : make_rsrc(p.D, 0);
+      const int lane = (int)__lane_id(), i = lane & 15, q = lane >> 4;
+      const uint32_t row = (uint32_t)(2 * ((c.wm * 128 + a * 16 + i) * p.No));
+#pragma unroll
+      for (int b = 0; b < FN; ++b) {
+        const int col = c.wn * 64 + b * 16 + 4 * q;
+        if constexpr (SWIGLU) r[b].x = (int)buf_load_u32(rr, row + (uint32_t)col);
+        else r[b] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rr, (int)(row + 2u * (uint32_t)col), 0, 0));
+      }
+    }
+  }
+
   // Row tile a of the finished tile.  Lane (i, q) holds row 16 a + i, columns
   // 16 b + 4 q .. + 3 of the wave's block.  Full tiles: lanes of different q
   // trade their packed pairs (v_permlane16_swap exchanges the odd 16-lane
   // rows of one register with the even rows of another, v_permlane32_swap
   // the halves) until each holds 16 contiguous bytes of its row.
-  __device__ static inline void store_rows(const Ctx &c, const Epi &e, int a, const v4i (&row)[FN]) {
+  __device__ static inline void store_rows(const Ctx &c, const Epi &e, int a, const v4i (&row)[FN],
+                                           const ResRow &res) {
     const Int8Args &p = *c.p;
     const int lane = (int)__lane_id(), i = lane & 15, q = lane >> 4;
     const uint32_t sc = c.lds0 + S_REG + (uint32_t)e.slot * SCALES;
@@ -245,15 +326,42 @@ struct Int8Loop {
       const uint32_t o = (uint32_t)(c.wn * 64 + b * 16 + 4 * q);
       const v4i s = *(const lds_v4i *)(uintptr_t)(sc + SB_OFF + o * 4);
       const v2i w = *(const lds_v2i *)(uintptr_t)(sc + BIAS_OFF + o * 2);
-      return int8_finish(row[b], sa, __builtin_bit_cast(v4f, s), unpack_bf16x4(w), ACT);
+      return int8_finish(row[b], sa, __builtin_bit_cast(v4f, s), unpack_bf16x4(w), RES ? (int)ACT_NONE : ACT);
     };
     if (e.full) {
       uint32_t rs = e.rowstride;
       asm volatile("" : "+s"(rs));
+      // two neighbouring 16-column blocks, 16 contiguous bytes per lane
+      auto put = [&](const v4f &x, const v4f &y, const u32x4 &rd, uint32_t voff, uint32_t soff) {
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x.z, x.w), pack_bf16x2(y.z, y.w), false, false);
+        store16_asm((v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]}, rd, voff, soff);
+      };
+      // the activation's argument, [M, N] whatever the activation
+      auto put_z = [&](const v4f &x, const v4f &y, int pr) {
+        const int64_t org = e.m0 * p.N + e.n0;
+        const int64_t r = c.wm * (FM * 16) + i;
+        put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))),
+            (uint32_t)(2 * (r * p.N + c.wn * 64 + 16 * (q & 1) + 8 * (q >> 1))), (uint32_t)(32 * p.N) * (uint32_t)a + 64u * pr);
+      };
       if constexpr (SWIGLU) {
         uint32_t d[4];
+        if constexpr (RES) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) d[b] = swiglu_pack(finish(b));
+          for (int pr = 0; pr < 2; ++pr) {
+            const v4f z[2] = {finish(2 * pr), finish(2 * pr + 1)};
+            if (p.Z) put_z(z[0], z[1], pr);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u = (uint32_t)res[2 * pr + k].x;
+              d[2 * pr + k] = pack_bf16x2(z[k].x * logistic_f32(z[k].x) * z[k].y + __uint_as_float(u << 16),
+                                          z[k].z * logistic_f32(z[k].z) * z[k].w + __uint_as_float(u & 0xFFFF0000u));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) d[b] = swiglu_pack(finish(b));
+        }
         // 4 x 4 transpose over (b, q)
         const auto s02 = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
         const auto s13 = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
@@ -263,17 +371,28 @@ struct Int8Loop {
       } else {
 #pragma unroll
         for (int pr = 0; pr < FN / 2; ++pr) {
-          const v4f x = finish(2 * pr), y = finish(2 * pr + 1);
-          const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y), false, false);
-          const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(x.z, x.w), pack_bf16x2(y.z, y.w), false, false);
-          store16_asm((v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]}, e.rd, e.voff, (uint32_t)a * rs + 64u * pr);
+          v4f x = finish(2 * pr), y = finish(2 * pr + 1);
+          if constexpr (RES) {
+            if (p.Z) put_z(x, y, pr);
+            const v4f rx = unpack_bf16x4(res[2 * pr]), ry = unpack_bf16x4(res[2 * pr + 1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = activate(ACT, x[k]) + rx[k];
+              y[k] = activate(ACT, y[k]) + ry[k];
+            }
+          }
+          put(x, y, e.rd, e.voff, (uint32_t)a * rs + 64u * pr);
         }
       }
     } else {
       const int64_t r = e.m0 + c.wm * (FM * 16) + a * 16 + i;
       if (r < e.lim) {
 #pragma unroll
-        for (int b = 0; b < FN; ++b) int8_store4(p, ACT, r, e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q, finish(b));
+        for (int b = 0; b < FN; ++b) {
+          const int64_t col = e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q;
+          if constexpr (RES) int8_emit4<true>(p, ACT, r, col, finish(b));
+          else int8_store4(p, ACT, r, col, finish(b));
+        }
       }
     }
   }
@@ -295,6 +414,11 @@ struct Int8Loop {
       b1[b] = lds_read16(base + ob1 + b * 2048);
     }
     v4i a0 = lds_read16(base + oa0), a1 = lds_read16(base + oa1);
+    // the residual of a row tile is loaded while the one before it is finished
+    ResRow res[2];
+    if constexpr (EPI && RES) {
+      if (e.on && e.full) load_residual(c, e, 0, res[0]);
+    }
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
       v4i n0, n1;
@@ -302,7 +426,12 @@ struct Int8Loop {
         n0 = lds_read16(base + oa0 + (a + 1) * 2048);
         n1 = lds_read16(base + oa1 + (a + 1) * 2048);
       }
-      if (EPI && e.on) store_rows(c, e, a, acc[a]);
+      if (EPI && e.on) {
+        if constexpr (RES) {
+          if (e.full && a + 1 < FM) load_residual(c, e, a + 1, res[(a + 1) & 1]);
+        }
+        store_rows(c, e, a, acc[a], res[a & 1]);
+      }
       // first operand = B tile: the result lane holds 4 consecutive n
 #pragma unroll
       for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(b0[b], a0, EPI ? (v4i){0, 0, 0, 0} : acc[a][b]);
@@ -386,14 +515,21 @@ struct Int8Loop {
         }
       }
     }
+    ResRow res[FM];
+    if constexpr (RES) {
+      if (e.full) {
 #pragma unroll
-    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a]);
+        for (int a = 0; a < FM; ++a) load_residual(c, e, a, res[a]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a], res[a]);
   }
 };
 
-template <int ACT>
+template <int ACT, bool RES = false>
 __global__ __launch_bounds__(DNW8 * 64, 1) void int8_tiled_kernel(Int8Args p) {
-  typedef Int8Loop<ACT> L;
+  typedef Int8Loop<ACT, RES> L;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::LDS_BYTES];
   __shared__ GroupTable gt;
   if (threadIdx.x < 64) int8_group_table<DBM>(p, gt, (int)threadIdx.x);
@@ -433,7 +569,7 @@ __global__ __launch_bounds__(DNW8 * 64, 1) void int8_tiled_kernel(Int8Args p) {
 // 128 x 4096 x 9600 27.9 and 31.0 us, 16 x 12000 x 9600 28 and 41, full rounds
 // 6 % slower; three stages and three workgroups per unit, 700 rows in 16
 // groups x 2048 x 4096 46 against 38.5 us.
-template <int BM, int BN, int KS, int NS>
+template <int BM, int BN, int KS, int NS, bool RES = false>
 __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
   constexpr int FM = BM / 32, FN = BN / 32, ABLK = BM / 32, BBLK = BN / 32;
   constexpr int AB = BM * 128, BB = BN * 128, STAGE = KS * (AB + BB);
@@ -572,8 +708,8 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
       if (r0 + a * 16 < t.lim) {
 #pragma unroll
         for (int b = 0; b < FN; ++b)
-          int8_store4(p, ACT, r0 + a * 16, t.n0 + wn * (BN / 2) + b * 16 + 4 * q,
-                      int8_finish(acc[a][b], sa, sb[b], bias[b], ACT));
+          int8_emit4<RES>(p, ACT, r0 + a * 16, t.n0 + wn * (BN / 2) + b * 16 + 4 * q,
+                          int8_finish(acc[a][b], sa, sb[b], bias[b], ACT_NONE));
       }
     }
   };
@@ -661,7 +797,7 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
 // Bound by memory where the weights are large (1 x 14336 x 4096: 12.0 us, 4.9
 // TB/s), else by a compute unit's 36 bytes per ns of 64-byte row pieces and
 // by latency (16 x 4096 x 4096 7.3 us, 13.8 through LDS in 64 x 64 tiles).
-template <int FM, int FN, int W, int U>
+template <int FM, int FN, int W, int U, bool RES = false>
 __global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args p) {
   constexpr int BM = 16 * FM, BN = 16 * FN;
   __shared__ v4i part[W][FM * FN][64];
@@ -744,12 +880,12 @@ __global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args p) {
     if (row < t.lim) {
       v4f sb, bias;
       int8_columns(p, t.g, t.n0, 16 * b + 4 * q, sb, bias);
-      int8_store4(p, p.act, row, col, int8_finish(sum, p.sA[row], sb, bias, p.act));
+      int8_emit4<RES>(p, p.act, row, col, int8_finish(sum, p.sA[row], sb, bias, ACT_NONE));
     }
   }
 }
 
-// K == 0: act(bias) in every row that belongs to a group.
+// K == 0: act(bias) in every row that belongs to a group, plus the residual.
 __global__ void int8_fill_kernel(Int8Args p) {
   int64_t covered = p.M;
   if (p.m_sizes) {
@@ -765,11 +901,14 @@ __global__ void int8_fill_kernel(Int8Args p) {
   auto bias = [&](int64_t n) { return p.bias ? __uint_as_float((uint32_t)p.bias[n] << 16) : 0.0f; };
   float z;
   if (p.act == ACT_SWIGLU) {
-    const float g = bias(2 * c);
-    z = g * logistic_f32(g) * bias(2 * c + 1);
+    const float g = bias(2 * c), u = bias(2 * c + 1);
+    z = g * logistic_f32(g) * u;
+    if (p.Z) ((uint32_t *)p.Z)[i] = pack_bf16x2(g, u);
   } else {
     z = activate(p.act, bias(c));
+    if (p.Z) p.Z[i] = (uint16_t)pack_bf16x2(bias(c), 0.0f);
   }
+  if (p.R) z += __uint_as_float((uint32_t)p.R[i] << 16);
   p.D[i] = (uint16_t)pack_bf16x2(z, 0.0f);
 }
 

@@ -2,7 +2,7 @@
 #include "kernels.hpp"
 
 namespace mxg {
-dense_fn pick_dense_fp4(int layout, bool psb, bool fuse) {
+dense_fn pick_dense_fp4(int layout, bool psb, int fuse) {
   return pick_big<F_E2M1, F_E2M1, SM_MX>(layout, psb, fuse);
 }
 }  // namespace mxg

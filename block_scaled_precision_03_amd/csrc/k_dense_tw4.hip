@@ -2,7 +2,7 @@
 #include "kernels.hpp"
 
 namespace mxg {
-dense_fn pick_dense_tw_a4(int eb, int layout, bool psb, bool fuse) {
+dense_fn pick_dense_tw_a4(int eb, int layout, bool psb, int fuse) {
   if (eb == F_E4M3) return pick_big<F_E4M3, F_E4M3, SM_TENSOR>(layout, psb, fuse);
   if (eb == F_E5M2) return pick_big<F_E4M3, F_E5M2, SM_TENSOR>(layout, psb, fuse);
   return nullptr;

@@ -83,6 +83,15 @@ int int8_variant(int G, int64_t M, int64_t N, int64_t K) {
   }
 }
 
+template <bool RES>
+void (*pick_tiled(int act))(Int8Args) {
+  return act == ACT_SWIGLU      ? int8_tiled_kernel<ACT_SWIGLU, RES>
+         : act == ACT_RELU      ? int8_tiled_kernel<ACT_RELU, RES>
+         : act == ACT_GELU_TANH ? int8_tiled_kernel<ACT_GELU_TANH, RES>
+         : act == ACT_SILU      ? int8_tiled_kernel<ACT_SILU, RES>
+                                : int8_tiled_kernel<ACT_NONE, RES>;
+}
+
 int launch(Int8Args &a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0 || a.No == 0) return MXG_OK;
   if (a.K == 0) {
@@ -99,30 +108,27 @@ int launch(Int8Args &a, hipStream_t stream) {
   void (*fn)(Int8Args);
   int64_t grid = 0;
   int threads = 256;
+  const bool res = a.R != nullptr || a.Z != nullptr;
   switch (k) {
     case ROWS16:
-      fn = int8_rows_kernel<1, 1, 4, 4>;
+      fn = res ? int8_rows_kernel<1, 1, 4, 4, true> : int8_rows_kernel<1, 1, 4, 4>;
       grid = (tiles + 7) / 8 * 8;          // eight bands (XCDs) of equal length
       break;
     case ROWS32:
-      fn = int8_rows_kernel<2, 2, 8, 2>;
+      fn = res ? int8_rows_kernel<2, 2, 8, 2, true> : int8_rows_kernel<2, 2, 8, 2>;
       grid = (tiles + 7) / 8 * 8;
       threads = 512;
       break;
     case STREAM64:
-      fn = int8_stream_kernel<64, 64, 1, 4>;
+      fn = res ? int8_stream_kernel<64, 64, 1, 4, true> : int8_stream_kernel<64, 64, 1, 4>;
       grid = std::min<int64_t>(tiles, 2ll * cu_count());
       break;
     case STREAM128:
-      fn = int8_stream_kernel<128, 128, 1, 2>;
+      fn = res ? int8_stream_kernel<128, 128, 1, 2, true> : int8_stream_kernel<128, 128, 1, 2>;
       grid = std::min<int64_t>(tiles, 2ll * cu_count());
       break;
     default:
-      fn = a.act == ACT_SWIGLU      ? int8_tiled_kernel<ACT_SWIGLU>
-           : a.act == ACT_RELU      ? int8_tiled_kernel<ACT_RELU>
-           : a.act == ACT_GELU_TANH ? int8_tiled_kernel<ACT_GELU_TANH>
-           : a.act == ACT_SILU      ? int8_tiled_kernel<ACT_SILU>
-                                    : int8_tiled_kernel<ACT_NONE>;
+      fn = res ? pick_tiled<true>(a.act) : pick_tiled<false>(a.act);
       grid = std::min<int64_t>(tiles, cu_count());
       threads = DNW8 * 64;
   }
@@ -158,7 +164,7 @@ int int8_dense_variant(int64_t M, int64_t N, int64_t K) {
 }
 
 int int8_run(const void *A, const void *sA, const void *B, const void *sB, void *D, int64_t M, int64_t N,
-             int64_t K, const void *bias, int act, hipStream_t stream) {
+             int64_t K, const void *bias, int act, const void *residual, void *z, hipStream_t stream) {
   Int8Args a = {};
   a.A = (const uint8_t *)A;
   a.B = (const uint8_t *)B;
@@ -172,6 +178,8 @@ int int8_run(const void *A, const void *sA, const void *B, const void *sB, void 
   a.No = act == MXG_ACT_SWIGLU ? N / 2 : N;
   a.G = 1;
   a.act = act;
+  a.R = (const uint16_t *)residual;
+  a.Z = (uint16_t *)z;
   return launch(a, stream);
 }
 

@@ -13,14 +13,17 @@ typedef void (*dense_fn)(DenseArgs);
 typedef void (*grouped_fn)(GroupedArgs);
 
 // Persistent 256 x 256 dense kernel of one scale mode (SM_MX, SM_TENSOR),
-// NT/NN/TN; `fuse`: the bias/activation epilogue (NT only).
+// NT/NN/TN; `fuse`: the epilogue, FUSE_* (NT only but for FUSE_NONE).
 template <int FA, int FB, int SMODE>
-dense_fn pick_big(int layout, bool psb, bool fuse) {
+dense_fn pick_big(int layout, bool psb, int fuse) {
   constexpr int NT = 0, NN = 1, TN = 2;          // the header's layout codes
-  if (fuse) {
+  if (fuse != FUSE_NONE) {
     if (layout != NT) return nullptr;
-    return psb ? dense_kernel<FA, FB, SMODE, false, false, true, true>
-               : dense_kernel<FA, FB, SMODE, false, false, false, true>;
+    if (fuse == FUSE_RES)
+      return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_RES>
+                 : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_RES>;
+    return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_ACT>
+               : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_ACT>;
   }
   {
     // MX scales are blocked along K whatever the code layout, so the
@@ -35,15 +38,15 @@ dense_fn pick_big(int layout, bool psb, bool fuse) {
 }
 
 // k_dense_mx4.hip / k_dense_mx5.hip: MX FP8 with A in E4M3 / E5M2.
-dense_fn pick_dense_mx_a4(int eb, int layout, bool psb, bool fuse);
-dense_fn pick_dense_mx_a5(int eb, int layout, bool psb, bool fuse);
+dense_fn pick_dense_mx_a4(int eb, int layout, bool psb, int fuse);
+dense_fn pick_dense_mx_a5(int eb, int layout, bool psb, int fuse);
 // k_dense_tw4.hip / k_dense_tw5.hip: tensor-wise FP8 with A in E4M3 / E5M2.
-dense_fn pick_dense_tw_a4(int eb, int layout, bool psb, bool fuse);
-dense_fn pick_dense_tw_a5(int eb, int layout, bool psb, bool fuse);
+dense_fn pick_dense_tw_a4(int eb, int layout, bool psb, int fuse);
+dense_fn pick_dense_tw_a5(int eb, int layout, bool psb, int fuse);
 // k_dense_fp4.hip: MXFP4.
-dense_fn pick_dense_fp4(int layout, bool psb, bool fuse);
+dense_fn pick_dense_fp4(int layout, bool psb, int fuse);
 // k_small.hip: the 64 x 64 NT kernel, every format.
-dense_fn pick_small(int ea, int eb, bool mx, bool psb, bool fuse);
+dense_fn pick_small(int ea, int eb, bool mx, bool psb, int fuse);
 // k_grouped.hip: the grouped kernels (256 x 256 dense pipeline; persistent
 // streaming with BM-row tiles; the streaming kernel on the dense pipeline's
 // tail pieces).

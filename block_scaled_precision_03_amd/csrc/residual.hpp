@@ -1,0 +1,144 @@
+// The gradient of the residual epilogue D = act(z) + R, z = sum + bias:
+//   dz = dD act'(z),  dbias[n] = sum_m dz[m,n]  (of the unrounded dz),
+// R's gradient being dD itself.  SwiGLU, D = g s(g) u with g = z[2j], u =
+// z[2j+1] and s the logistic function: dg = dD u s (1 + g (1 - s)), du = dD g s.
+//
+// A stream over dD, z and dz; the column sums are formed beside it: a
+// workgroup walks the rows of its part for its columns and leaves FP32
+// partial sums in the workspace, which a second kernel adds in order.
+#pragma once
+#include "common.hpp"
+
+namespace mxg {
+
+struct ResidualGradArgs {
+  const uint16_t *dD;              // [M, No]
+  const uint16_t *z;               // [M, N]
+  uint16_t *dz;                    // [M, N] or null
+  float *part;                     // [parts, N] or null (no bias gradient)
+  int64_t M, N, No, rows;          // rows per part
+};
+
+// act'(z).
+//   GELU (tanh form): z s(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
+//     s + z s (1 - s) 2u',  u' = sqrt(2/pi) (1 + 0.134145 z^2)
+//   SiLU: s + z s (1 - s)
+// 1 - s is formed as the logistic function of the negated argument, which
+// keeps its leading bits where s is near 1, and z s (1 - s) as 0 where it
+// vanishes (|z| large), not as infinity times zero.
+template <int ACT>
+__device__ inline float act_slope(float z) {
+  if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (ACT == ACT_GELU_TANH) {
+    const float c = fminf(fmaxf(z, -16.0f), 16.0f);        // beyond: exactly 0 or 1
+    const float u2 = 1.5957691216057308f * fmaf(0.044715f * c, c * c, c);
+    const float s = logistic_f32(u2), t = logistic_f32(-u2);
+    const float d = fmaf(c * s * t, 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f), s);
+    return z == z ? d : z;
+  }
+  if constexpr (ACT == ACT_SILU) {
+    const float c = fminf(fmaxf(z, -126.0f), 126.0f);
+    const float s = logistic_f32(c), t = logistic_f32(-c);
+    const float d = fmaf(c * s, t, s);
+    return z == z ? d : z;
+  }
+  return 1.0f;
+}
+
+// N BF16 values of a row of which `room` are left, at any alignment (an odd
+// pitch leaves rows at two bytes; the hardware takes any).
+template <int N>
+__device__ inline void load_row(const uint16_t *src, int64_t room, float (&v)[N]) {
+  uint16_t h[N];
+  if (room >= N) {
+    __builtin_memcpy(h, src, 2 * N);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) h[k] = k < room ? src[k] : (uint16_t)0;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __uint_as_float((uint32_t)h[k] << 16);
+}
+
+// Eight columns of z per lane, four rows at a time (their loads in flight
+// together); block (x, y): columns 512 x .., the rows of part y, row r of them
+// to wave r % 4.
+constexpr int RG_VEC = 8, RG_COLS = 64 * RG_VEC, RG_ROWS = 4;
+
+template <int ACT>
+__global__ __launch_bounds__(256) void residual_grad_kernel(ResidualGradArgs p) {
+  constexpr bool GATED = ACT == ACT_SWIGLU;
+  constexpr int V = RG_VEC, DV = GATED ? V / 2 : V;
+  __shared__ float sums[4][RG_COLS];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * RG_COLS + lane * V, room = p.N - c;
+  const int64_t cd = GATED ? c / 2 : c, roomd = GATED ? room / 2 : room;
+  const int64_t m0 = (int64_t)blockIdx.y * p.rows, m1 = min(p.M, m0 + p.rows);
+  float sum[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum[k] = 0.0f;
+  if (room > 0) {
+    for (int64_t m = m0 + w; m < m1; m += 4 * RG_ROWS) {
+      float d[RG_ROWS][DV], z[RG_ROWS][V];
+#pragma unroll
+      for (int i = 0; i < RG_ROWS; ++i) {
+        const int64_t r = m + 4 * i;
+        if (r < m1) {
+          load_row<DV>(p.dD + r * p.No + cd, roomd, d[i]);
+          if constexpr (ACT != ACT_NONE) load_row<V>(p.z + r * p.N + c, room, z[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RG_ROWS; ++i) {
+        const int64_t r = m + 4 * i;
+        if (r >= m1) break;
+        float g[V];
+        if constexpr (GATED) {
+#pragma unroll
+          for (int k = 0; k < DV; ++k) {
+            const float a = z[i][2 * k], u = z[i][2 * k + 1];
+            g[2 * k] = d[i][k] * (u * act_slope<ACT_SILU>(a));
+            g[2 * k + 1] = d[i][k] * (a * logistic_f32(a));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) g[k] = ACT == ACT_NONE ? d[i][k] : d[i][k] * act_slope<ACT>(z[i][k]);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum[k] += g[k];
+        if (p.dz) {
+          uint32_t o[V / 2];
+#pragma unroll
+          for (int k = 0; k < V / 2; ++k) o[k] = pack_bf16x2(g[2 * k], g[2 * k + 1]);
+          uint16_t *dst = p.dz + r * p.N + c;
+          if (room >= V) {
+            __builtin_memcpy(dst, o, 2 * V);
+          } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+              if (k < room) dst[k] = (uint16_t)(o[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sums[w][lane * V + k] = sum[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < RG_COLS; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * RG_COLS + i;
+    if (col < p.N) p.part[(int64_t)blockIdx.y * p.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+  }
+}
+
+// out[n] = sum of the parts, in order; none: 0.
+__global__ __launch_bounds__(256) void column_sums_kernel(const float *part, float *out, int64_t N, int parts) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.0f;
+  for (int k = 0; k < parts; ++k) s += part[(int64_t)k * N + n];
+  out[n] = s;
+}
+
+}  // namespace mxg

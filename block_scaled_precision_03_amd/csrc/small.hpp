@@ -26,7 +26,32 @@ namespace mxg {
 
 constexpr int SBM = 64, SBN = 64;
 
-template <int FA, int FB, int SMODE, bool PSB, bool FUSE>
+// Four consecutive values of a BF16 row of which `room` are left (8-byte
+// accesses where the row pitch allows, `wide`).
+__device__ inline void store_bf16x4(uint16_t *dst, const v4f &v, int64_t room, bool wide) {
+  const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+  if (room >= 4 && wide) {
+    *(v2i *)dst = (v2i){(int)u[0], (int)u[1]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < room) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
+  }
+}
+__device__ inline v4f load_bf16x4(const uint16_t *src, int64_t room, bool wide) {
+  if (room >= 4 && wide) {
+    const v2i u = *(const v2i *)src;
+    return (v4f){__uint_as_float((uint32_t)u.x << 16), __uint_as_float((uint32_t)u.x & 0xFFFF0000u),
+                 __uint_as_float((uint32_t)u.y << 16), __uint_as_float((uint32_t)u.y & 0xFFFF0000u)};
+  }
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < room) v[k] = __uint_as_float((uint32_t)src[k] << 16);
+  return v;
+}
+
+template <int FA, int FB, int SMODE, bool PSB, int FUSE>
 __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs p) {
   constexpr bool FP4 = (FA == F_E2M1);
   constexpr bool MX = (SMODE == SM_MX);
@@ -166,20 +191,19 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs p) {
           for (int k = 0; k < 4; ++k)
             if (col + k < p.N) bias[k] = __uint_as_float((uint32_t)p.bias[col + k] << 16);
         }
-        v.x = activate(p.act, v.x + bias[0]);
-        v.y = activate(p.act, v.y + bias[1]);
-        v.z = activate(p.act, v.z + bias[2]);
-        v.w = activate(p.act, v.w + bias[3]);
+        v += (v4f){bias[0], bias[1], bias[2], bias[3]};
+        if constexpr (FUSE == FUSE_RES) {
+          if (p.Z) store_bf16x4(p.Z + r * p.N + col, v, p.N - col, (p.N & 3) == 0);
+        }
+        v.x = activate(p.act, v.x);
+        v.y = activate(p.act, v.y);
+        v.z = activate(p.act, v.z);
+        v.w = activate(p.act, v.w);
+        if constexpr (FUSE == FUSE_RES) {
+          if (p.R) v += load_bf16x4(p.R + r * p.N + col, p.N - col, (p.N & 3) == 0);
+        }
       }
-      const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-      uint16_t *dst = p.D + r * p.N + col;
-      if (col + 4 <= p.N && (p.N & 3) == 0) {
-        *(v2i *)dst = (v2i){(int)u[0], (int)u[1]};
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (col + k < p.N) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
-      }
+      store_bf16x4(p.D + r * p.N + col, v, p.N - col, (p.N & 3) == 0);
     }
   }
 }

@@ -42,6 +42,8 @@ EXPORTS = (
     "grouped_int8_gemm_run", "grouped_int8_gemm_validate", "grouped_int8_gemm_variant", "mxgemm_quantize_int8",
     "moe_route_workspace_bytes", "moe_route", "moe_route_backward", "moe_combine", "moe_combine_backward",
     "moe_experts_workspace_bytes", "moe_experts", "moe_experts_validate",
+    "mxgemm_run_residual", "mxgemm_validate_residual", "mxgemm_residual_backward_workspace_bytes",
+    "mxgemm_residual_backward", "mxgemm_residual_backward_validate",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -133,6 +135,16 @@ _lib.moe_experts.restype = _i
 _lib.moe_experts.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i64, _i64, _i, _p, _i64, _p]
 _lib.moe_experts_validate.restype = _i
 _lib.moe_experts_validate.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i64, _i64, _i, _p, _i64]
+_lib.mxgemm_run_residual.restype = _i
+_lib.mxgemm_run_residual.argtypes = [_i, _i, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i, _p, _p, _p]
+_lib.mxgemm_validate_residual.restype = _i
+_lib.mxgemm_validate_residual.argtypes = [_i, _i, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i, _p, _p]
+_lib.mxgemm_residual_backward_workspace_bytes.restype = _i64
+_lib.mxgemm_residual_backward_workspace_bytes.argtypes = [_i64, _i64]
+_lib.mxgemm_residual_backward.restype = _i
+_lib.mxgemm_residual_backward.argtypes = [_i, _p, _p, _p, _p, _i64, _i64, _p, _i64, _p]
+_lib.mxgemm_residual_backward_validate.restype = _i
+_lib.mxgemm_residual_backward_validate.argtypes = [_i, _p, _p, _p, _p, _i64, _i64, _p, _i64]
 
 
 class MxgemmError(RuntimeError):
@@ -438,3 +450,36 @@ def moe_experts_validate(fmt, x, ids, weights, w1, s1, w2, s2, out, T, E, topk, 
     ws, nbytes = _workspace(workspace, lambda: _lib.moe_experts_workspace_bytes(T, topk, F))
     return _lib.moe_experts_validate(fmt, _ptr(x), _ptr(ids), _ptr(weights), _ptr(w1), _ptr(s1), _ptr(w2), _ptr(s2),
                                      _ptr(residual), _ptr(out), T, E, topk, D, F, activation, ws, nbytes)
+
+
+def run_residual(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias=None, activation=ACT_NONE, residual=None, z=None,
+                 stream=None):
+    """D = act(sum_k a(m,k) b(n,k) + bias[n]) + residual in BF16, the
+    activation's argument to z where given (see include/mxgemm.h)."""
+    _check(_lib.mxgemm_run_residual(fmtA, fmtB, layout, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(D), M, N, K,
+                                    _ptr(bias), activation, _ptr(residual), _ptr(z), _stream(stream)),
+           "mxgemm_run_residual")
+
+
+def validate_residual(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias=None, activation=ACT_NONE, residual=None,
+                      z=None):
+    return _lib.mxgemm_validate_residual(fmtA, fmtB, layout, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(D), M, N, K,
+                                         _ptr(bias), activation, _ptr(residual), _ptr(z))
+
+
+def residual_backward_workspace_bytes(M, N):
+    return _lib.mxgemm_residual_backward_workspace_bytes(M, N)
+
+
+def residual_backward(activation, dD, z, dz, dbias, M, N, workspace=None, stream=None):
+    """Gradient of run_residual's epilogue: dz = dD act'(z) and dbias [N] =
+    its column sums, either may be None; workspace (for dbias): a device
+    tensor of residual_backward_workspace_bytes(M, N) bytes or more."""
+    ws, nbytes = _workspace(workspace, lambda: _lib.mxgemm_residual_backward_workspace_bytes(M, N))
+    _check(_lib.mxgemm_residual_backward(activation, _ptr(dD), _ptr(z), _ptr(dz), _ptr(dbias), M, N, ws, nbytes,
+                                         _stream(stream)), "mxgemm_residual_backward")
+
+
+def residual_backward_validate(activation, dD, z, dz, dbias, M, N, workspace=None):
+    ws, nbytes = _workspace(workspace, lambda: _lib.mxgemm_residual_backward_workspace_bytes(M, N))
+    return _lib.mxgemm_residual_backward_validate(activation, _ptr(dD), _ptr(z), _ptr(dz), _ptr(dbias), M, N, ws, nbytes)

@@ -27,12 +27,13 @@
  * Conventions for every entry point:
  *  - All data pointers are DEVICE pointers owned by the caller.  The library
  *    never allocates, frees or retains caller memory and uses no workspace
- *    (moe_route and moe_experts take one from the caller; see there).
+ *    (moe_route, moe_experts and mxgemm_residual_backward take one from the
+ *    caller; see there).
  *  - Calls are stream-ordered and asynchronous: exactly one kernel is
  *    enqueued on `stream` (0 = the null stream) per successful call, with
  *    these exceptions: mxgemm_quantize_tensor enqueues four (its scale output
  *    serves as the amax word between them; see there), moe_route at most
- *    two (see there), moe_experts two, and
+ *    two (see there), moe_experts two, mxgemm_residual_backward at most two, and
  *    grouped_fp8_gemm_run and grouped_bf16_gemm_run enqueue two when they
  *    run MXG_GROUPED_TILED on more 256 x 256 tiles than the device has
  *    compute units (see grouped_fp8_gemm_variant).  The tuning call grouped_fp8_gemm_autotune
@@ -718,6 +719,56 @@ int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float
                          const void *s1, const void *w2, const void *s2, const void *residual, const void *out,
                          int64_t T, int64_t E, int topk, int64_t D, int64_t F, int activation, const void *workspace,
                          int64_t workspace_bytes);
+
+/*
+ * mxgemm_run_residual -- mxgemm_run_fused with a residual in its epilogue, and
+ * what the epilogue's gradient needs:
+ *
+ *   z = sum_k a(m,k) b(n,k) + bias[n],   D = act(z) + residual
+ *
+ * in FP32, rounded once to BF16.  Arguments, formats and limits as
+ * mxgemm_run_fused (MXG_NT; MXG_ACT_SWIGLU with MXG_INT8 alone, D then
+ * [M, N/2]), and:
+ * residual  BF16, the shape of D, 16-byte aligned, or NULL; it may be the same
+ *         buffer as D (a layer's residual stream updated in place).
+ * z       BF16 out [M, N], the activation's argument (with MXG_ACT_SWIGLU too
+ *         [M, N]), 16-byte aligned, or NULL; no other argument's buffer.
+ * With neither it is mxgemm_run_fused.  K = 0: z = bias.  Sums may be formed
+ * in another order than mxgemm_run's (few rows split K over waves), so the two
+ * can differ in the last bit.
+ * Errors as mxgemm_run_fused; z the same pointer as D or residual is
+ * MXG_ERR_INVALID_ARG.
+ *
+ * mxgemm_residual_backward -- the epilogue's gradient: from dD (D's gradient,
+ * which is the residual's too)
+ *   dz[m,n] = dD[m,n] act'(z[m,n]),   dbias[n] = sum_m dz[m,n]
+ * (MXG_ACT_SWIGLU, D = g s(g) u: dg = dD u s(g) (1 + g (1 - s(g))), du = dD g
+ * s(g) at columns 2j and 2j + 1).
+ * dD      BF16 [M, N], with MXG_ACT_SWIGLU [M, N/2] and N even; z BF16 [M, N]
+ *         (not read with MXG_ACT_NONE).
+ * dz      BF16 out [M, N] or NULL; it may be z's buffer or (not SwiGLU) dD's.
+ * dbias   FP32 out [N] or NULL: FP32 sums of the unrounded dz in an order that
+ *         the sizes alone decide (the same call gives the same bits); M = 0
+ *         gives zeros.
+ * workspace, workspace_bytes  for dbias: 16-byte aligned device memory of at
+ *         least mxgemm_residual_backward_workspace_bytes(M, N) bytes (0 for few
+ *         rows), free once the call's work is done.
+ * dD, z, dz 16-byte aligned; M, N < 2^31.  ReLU's slope at 0 is 0.  At most two
+ * kernels.  N = 0: no-op.  Neither dz nor dbias, or a small workspace, is
+ * MXG_ERR_INVALID_ARG.
+ */
+int mxgemm_run_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
+                        void *D, int64_t M, int64_t N, int64_t K, const void *bias, int activation,
+                        const void *residual, void *z, hipStream_t stream);
+int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B,
+                             const void *sB, const void *D, int64_t M, int64_t N, int64_t K, const void *bias,
+                             int activation, const void *residual, const void *z);
+int64_t mxgemm_residual_backward_workspace_bytes(int64_t M, int64_t N);
+int mxgemm_residual_backward(int activation, const void *dD, const void *z, void *dz, float *dbias, int64_t M,
+                             int64_t N, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int mxgemm_residual_backward_validate(int activation, const void *dD, const void *z, const void *dz,
+                                      const float *dbias, int64_t M, int64_t N, const void *workspace,
+                                      int64_t workspace_bytes);
 
 #ifdef __cplusplus
 }
