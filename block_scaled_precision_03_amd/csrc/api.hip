@@ -19,6 +19,7 @@
 #include "kernels.hpp"
 #include "preshuffle.hpp"
 #include "quant.hpp"
+#include "rows.hpp"
 #include "diag.hpp"
 
 using namespace mxg;
@@ -45,6 +46,7 @@ FmtInfo fmt_info(int f) {
 // Largest operand extents the 32-bit in-kernel offsets support.
 constexpr int64_t MAX_ROW_BYTES = 1ll << 22;   // bytes of K per row (256 rows < 2^30)
 constexpr int64_t MAX_T_BYTES = 0x7FFFFFF0ll;   // a transposed operand, whole
+constexpr int64_t MAX_RES_COLS = 1 << 22;      // residual epilogue: 256 rows < 2^31 bytes
 constexpr int64_t MAX_PSB_BYTES = (1ll << 32) - (1ll << 16);   // a preshuffled B, whole
 
 // The persistent grouped kernels run GS_OCC workgroups per compute unit (74
@@ -151,10 +153,33 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
   return MXG_OK;
 }
 
+// Kernel choice of the residual epilogue: those of mxgemm_dense_variant, and
+// the kernels for few rows.
+namespace {
+// Row tiles of the kernels for few rows: 16, 32 or 64 rows.
+int rows_fm(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+
+bool few_rows(int fmtA, int64_t M, int64_t N, int64_t K) {
+  return M <= 64;
+}
+}  // namespace
+
+extern "C" int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
+  if (layout == MXG_NT && M > 0 && N > 0 && K > 0 && fmtA != MXG_INT8 && few_rows(fmtA, M, N, K)) return MXG_DENSE_ROWS;
+  return mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+}
+
 namespace {
 // Kernel selection for the dense path (the instantiations live in the k_*.hip
 // translation units).
 dense_fn pick_dense(int ea, int eb, bool mx, int layout, bool psb, int fuse) {
+  if (fuse == FUSE_RES || fuse == FUSE_RES_ACT) {
+    if (layout != MXG_NT) return nullptr;
+    if (ea == F_E2M1 || eb == F_E2M1) return ea == eb && mx ? pick_residual_fp4(psb, fuse) : nullptr;
+    if (ea == F_E4M3) return mx ? pick_residual_mx_a4(eb, psb, fuse) : pick_residual_tw_a4(eb, psb, fuse);
+    if (ea == F_E5M2) return mx ? pick_residual_mx_a5(eb, psb, fuse) : pick_residual_tw_a5(eb, psb, fuse);
+    return nullptr;
+  }
   if (ea == F_E2M1 || eb == F_E2M1)
     return (ea == F_E2M1 && eb == F_E2M1 && mx) ? pick_dense_fp4(layout, psb, fuse) : nullptr;
   if (ea == F_E4M3) return mx ? pick_dense_mx_a4(eb, layout, psb, fuse) : pick_dense_tw_a4(eb, layout, psb, fuse);
@@ -183,8 +208,9 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
               void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, const void *residual, void *z,
               hipStream_t stream) {
   if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, residual, z, stream);
-  const int fuse = residual != nullptr || z != nullptr ? FUSE_RES
-                   : bias != nullptr || act != MXG_ACT_NONE ? FUSE_ACT : FUSE_NONE;
+  const int fuse = residual != nullptr || z != nullptr        ? (act != MXG_ACT_NONE ? FUSE_RES_ACT : FUSE_RES)
+                   : bias != nullptr || act != MXG_ACT_NONE ? FUSE_ACT
+                                                            : FUSE_NONE;
   if (M == 0 || N == 0) return MXG_OK;
   if (K == 0) {
     const int64_t n = M * N;
@@ -198,8 +224,13 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   }
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  const bool small = mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64;
-  dense_fn fn = small ? pick_small(fa.elem, fb.elem, fa.mx, psb, fuse) : pick_dense(fa.elem, fb.elem, fa.mx, layout, psb, fuse);
+  const int variant = fuse >= FUSE_RES ? mxgemm_residual_variant(fmtA, fmtB, layout, M, N, K)
+                                       : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+  const bool small = variant == MXG_DENSE_TILE64, rows = variant == MXG_DENSE_ROWS;
+  const int fm = rows_fm(M);
+  dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, fm)
+                : small ? pick_small(fa.elem, fb.elem, fa.mx, psb, fuse)
+                        : pick_dense(fa.elem, fb.elem, fa.mx, layout, psb, fuse);
   if (!fn) return MXG_ERR_UNSUPPORTED;
   const bool fp4 = fa.elem == F_E2M1;
   DenseArgs a = {};
@@ -215,14 +246,18 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   a.b_bytes = psb ? mxgemm_preshuffle_b_bytes(fmtB & ~MXG_PRESHUFFLED, N, K) : (fp4 ? N * K / 2 : N * K);
   a.sa_bytes = fa.mx ? M * (K / 32) : 4;
   a.sb_bytes = fb.mx ? (psb ? mxgemm_preshuffle_scales_bytes(N, K) : N * (K / 32)) : 4;
-  a.tiles_m = (int)cdiv(M, small ? SBM : DBM);
-  a.tiles_n = (int)cdiv(N, small ? SBN : DBN);
+  a.tiles_m = (int)cdiv(M, rows ? 16 * fm : small ? SBM : DBM);
+  a.tiles_n = (int)cdiv(N, rows ? (fm == 1 ? 16 : 32) : small ? SBN : DBN);
   a.bias = (const uint16_t *)bias;
   a.act = act;
   a.R = (const uint16_t *)residual;
   a.Z = (uint16_t *)z;
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   if (tiles > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
+  if (rows) {
+    hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(64 * ROWS_WAVES), 0, stream, a);
+    return launch_status();
+  }
   if (small) {
     // one workgroup of four waves per 64 x 64 tile
     hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(256), 0, stream, a);
@@ -276,6 +311,8 @@ extern "C" int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const vo
   if (v != MXG_OK) return v;
   if (residual == nullptr && z == nullptr) return MXG_OK;
   if (layout != MXG_NT) return MXG_ERR_UNSUPPORTED;
+  // the residual kernels address a tile's rows with one 32-bit offset
+  if (N > MAX_RES_COLS) return MXG_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MXG_OK;
   if (z != nullptr && (z == D || z == residual)) return MXG_ERR_INVALID_ARG;
   if (!aligned(residual, 16) || !aligned(z, 16)) return MXG_ERR_MISALIGNED;

@@ -202,6 +202,16 @@ __device__ inline float activate(int act, float z) {
   return z;
 }
 
+// activate() without branches, the same bits: SiLU and GELU are both z times a
+// logistic function, so that one of them serves every activation.  For code
+// that repeats it often: the branches of activate(), 128 times over, made a
+// dense kernel too large for its loops to be unrolled.
+__device__ inline float activate_select(int act, float z) {
+  const float u = 0.7978845608028654f * fmaf(0.044715f * z, z * z, z);
+  const float gated = z * logistic_f32(act == ACT_GELU_TANH ? 2.0f * u : z);
+  return act == ACT_NONE ? z : act == ACT_RELU ? fmaxf(z, 0.0f) : gated;
+}
+
 // Workgroup index of a grid that the host folds into rows of 2^20 (flat_grid):
 // a dimension holds fewer than 2^32 work-items.
 constexpr int FLAT_LOG2 = 20;

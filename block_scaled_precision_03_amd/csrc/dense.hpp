@@ -51,9 +51,9 @@ struct DenseArgs {
 };
 
 // What a dense kernel does to a finished sum before its rounding to BF16:
-// nothing; bias and activation; bias, activation, residual (and the
-// activation's argument stored beside the result).
-enum : int { FUSE_NONE = 0, FUSE_ACT = 1, FUSE_RES = 2 };
+// nothing; bias and activation; bias and residual (and the activation's
+// argument stored beside the result), without and with an activation.
+enum : int { FUSE_NONE = 0, FUSE_ACT = 1, FUSE_RES = 2, FUSE_RES_ACT = 3 };
 
 // One output tile: origin, the row limit of its stores (M, or the end of its
 // group) and, for the grouped GEMM, its group (index, first row, rows).
@@ -128,7 +128,7 @@ __device__ inline void wait_vmem_le() {
 //
 template <int FA, int FB, int SMODE, bool TA, bool TB, bool PSB, int FUSE = FUSE_NONE>
 struct DenseLoop {
-  static constexpr bool RES = FUSE == FUSE_RES;
+  static constexpr bool RES = FUSE == FUSE_RES || FUSE == FUSE_RES_ACT;
   static constexpr bool FP4 = (FA == F_E2M1);
   static constexpr bool MX = (SMODE == SM_MX);
   static constexpr bool GROUP = (SMODE == SM_GROUP);
@@ -575,7 +575,7 @@ struct DenseLoop {
     e.n0 = (int)n0;
     e.lim = (int)lim;
     e.bslot = bslot;
-    e.act = FUSE ? p.act : ACT_NONE;
+    e.act = FUSE != FUSE_NONE && FUSE != FUSE_RES ? p.act : ACT_NONE;
     e.alpha = alpha;
     e.on = on;
     // Full tiles store through the range-checked vector offset (at most
@@ -601,7 +601,9 @@ struct DenseLoop {
       const int64_t org = (int64_t)e.m0 * p.N + e.n0;
       const __amdgpu_buffer_rsrc_t rr =
           p.R ? make_rsrc(p.R + org, clamp_records(2 * (p.M * p.N - org))) : make_rsrc(p.D, 0);
-      const int lane = (int)__lane_id(), i = lane & 15, q = lane >> 4;
+      int lane = (int)__lane_id();
+      asm volatile("" : "+v"(lane));       // the offset formed here, not kept
+      const int i = lane & 15, q = lane >> 4;
       const uint32_t o = (uint32_t)(2 * ((c.wm * (FM * 16) + a * 16 + i) * p.N + c.wn * (FN * 16) + 4 * q));
 #pragma unroll
       for (int b = 0; b < FN; ++b)
@@ -633,7 +635,11 @@ struct DenseLoop {
     };
     // The activation (and the residual) after it.
     auto activated = [&](v4f v, const v2i &r) -> v4f {
-      if constexpr (FUSE) {
+      if constexpr (FUSE == FUSE_RES_ACT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = activate_select(e.act, v[k]);
+      }
+      if constexpr (FUSE == FUSE_ACT) {
         const int act = e.act;
         if (act != ACT_NONE) {
           v.x = activate(act, v.x);
@@ -682,6 +688,39 @@ struct DenseLoop {
           put(activated(x, v2i{}), activated(y, v2i{}), e.rd, pr);
         }
       }
+    } else if constexpr (RES) {
+      // edge tiles, element by element through range-checked offsets (N is at
+      // most 2^22): those of no row or column go past any resource
+      const DenseArgs &p = *c.p;
+      int lane = (int)__lane_id();
+      asm volatile("" : "+v"(lane));       // offsets formed here, not kept from row tile to row tile
+      const int i = lane & 15, q = lane >> 4;
+      const int64_t org = (int64_t)e.m0 * p.N + e.n0;
+      const uint32_t left = clamp_records(2 * (p.M * p.N - org));
+      const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + org, left);
+      const __amdgpu_buffer_rsrc_t rr = p.R ? make_rsrc(p.R + org, left) : make_rsrc(p.D, 0);
+      const __amdgpu_buffer_rsrc_t rz = p.Z ? make_rsrc(p.Z + org, left) : make_rsrc(p.D, 0);
+      const int r = c.wm * (FM * 16) + a * 16 + i;
+      const bool in = (int64_t)e.m0 + r < e.lim;
+#pragma unroll
+      for (int b = 0; b < FN; ++b) {
+        const int col = c.wn * (FN * 16) + b * 16 + 4 * q;
+        uint32_t o[4], near[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[k] = in && e.n0 + col + k < p.N ? (uint32_t)(2 * (r * p.N + col + k)) : 0x80000000u;
+          near[k] = __builtin_amdgcn_raw_buffer_load_b16(rr, (int)o[k], 0, 0);
+        }
+        const v4f z = finish(row[b], b);
+        const v4f v = activated(z, (v2i){(int)(near[0] | near[1] << 16), (int)(near[2] | near[3] << 16)});
+        const uint32_t uz[2] = {pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w)};
+        const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(uz[k >> 1] >> (16 * (k & 1))), rz, (int)o[k], 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(u[k >> 1] >> (16 * (k & 1))), rd, (int)o[k], 0, 0);
+        }
+      }
     } else {
       // edge tiles: lane position recomputed here rather than kept live
       const DenseArgs &p = *c.p;
@@ -691,26 +730,9 @@ struct DenseLoop {
         uint16_t *dst = p.D + r * p.N;
 #pragma unroll
         for (int b = 0; b < FN; ++b) {
-          const v4f z = finish(row[b], b);
-          const int64_t col = (int64_t)e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q;
-          v2i near = {0, 0};
-          if constexpr (RES) {
-            if (p.R) {
-              uint16_t h[4] = {0, 0, 0, 0};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (col + k < p.N) h[k] = p.R[r * p.N + col + k];
-              near = (v2i){(int)(h[0] | (uint32_t)h[1] << 16), (int)(h[2] | (uint32_t)h[3] << 16)};
-            }
-            if (p.Z) {
-              const uint32_t uz[2] = {pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w)};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (col + k < p.N) p.Z[r * p.N + col + k] = (uint16_t)(uz[k >> 1] >> (16 * (k & 1)));
-            }
-          }
-          const v4f v = activated(z, near);
+          const v4f v = activated(finish(row[b], b), v2i{});
           const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+          const int64_t col = (int64_t)e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (col + k < p.N) dst[col + k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));

@@ -300,7 +300,9 @@ struct Int8Loop {
       const int64_t org = e.m0 * p.No + (SWIGLU ? e.n0 / 2 : e.n0);
       const __amdgpu_buffer_rsrc_t rr =
           p.R ? make_rsrc(p.R + org, clamp_records(2 * (p.M * p.No - org))) : make_rsrc(p.D, 0);
-      const int lane = (int)__lane_id(), i = lane & 15, q = lane >> 4;
+      int lane = (int)__lane_id();
+      asm volatile("" : "+v"(lane));       // the offset formed here, not kept from row tile to row tile
+      const int i = lane & 15, q = lane >> 4;
       const uint32_t row = (uint32_t)(2 * ((c.wm * 128 + a * 16 + i) * p.No));
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
@@ -340,7 +342,9 @@ struct Int8Loop {
       // the activation's argument, [M, N] whatever the activation
       auto put_z = [&](const v4f &x, const v4f &y, int pr) {
         const int64_t org = e.m0 * p.N + e.n0;
-        const int64_t r = c.wm * (FM * 16) + i;
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int64_t r = c.wm * (FM * 16) + (l & 15);
         put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))),
             (uint32_t)(2 * (r * p.N + c.wn * 64 + 16 * (q & 1) + 8 * (q >> 1))), (uint32_t)(32 * p.N) * (uint32_t)a + 64u * pr);
       };

@@ -6,12 +6,12 @@ namespace {
 template <int FA, int FB>
 dense_fn pick_small_fmt(bool mx, bool psb, int fuse) {
   if (mx) {
-    if (fuse == FUSE_RES) return psb ? dense_small_kernel<FA, FB, SM_MX, true, FUSE_RES> : dense_small_kernel<FA, FB, SM_MX, false, FUSE_RES>;
+    if (fuse == FUSE_RES || fuse == FUSE_RES_ACT) return psb ? dense_small_kernel<FA, FB, SM_MX, true, FUSE_RES> : dense_small_kernel<FA, FB, SM_MX, false, FUSE_RES>;
     if (fuse) return psb ? dense_small_kernel<FA, FB, SM_MX, true, FUSE_ACT> : dense_small_kernel<FA, FB, SM_MX, false, FUSE_ACT>;
     return psb ? dense_small_kernel<FA, FB, SM_MX, true, FUSE_NONE> : dense_small_kernel<FA, FB, SM_MX, false, FUSE_NONE>;
   }
   if constexpr (FA != F_E2M1 && FB != F_E2M1) {
-    if (fuse == FUSE_RES)
+    if (fuse == FUSE_RES || fuse == FUSE_RES_ACT)
       return psb ? dense_small_kernel<FA, FB, SM_TENSOR, true, FUSE_RES> : dense_small_kernel<FA, FB, SM_TENSOR, false, FUSE_RES>;
     if (fuse)
       return psb ? dense_small_kernel<FA, FB, SM_TENSOR, true, FUSE_ACT> : dense_small_kernel<FA, FB, SM_TENSOR, false, FUSE_ACT>;

@@ -13,15 +13,12 @@ typedef void (*dense_fn)(DenseArgs);
 typedef void (*grouped_fn)(GroupedArgs);
 
 // Persistent 256 x 256 dense kernel of one scale mode (SM_MX, SM_TENSOR),
-// NT/NN/TN; `fuse`: the epilogue, FUSE_* (NT only but for FUSE_NONE).
+// NT/NN/TN; `fuse`: FUSE_NONE or (NT only) FUSE_ACT.
 template <int FA, int FB, int SMODE>
 dense_fn pick_big(int layout, bool psb, int fuse) {
   constexpr int NT = 0, NN = 1, TN = 2;          // the header's layout codes
   if (fuse != FUSE_NONE) {
     if (layout != NT) return nullptr;
-    if (fuse == FUSE_RES)
-      return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_RES>
-                 : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_RES>;
     return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_ACT>
                : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_ACT>;
   }
@@ -37,6 +34,16 @@ dense_fn pick_big(int layout, bool psb, int fuse) {
   }
 }
 
+// The same with the residual epilogue (NT only), FUSE_RES or FUSE_RES_ACT.
+template <int FA, int FB, int SMODE>
+dense_fn pick_residual(bool psb, int fuse) {
+  if (fuse == FUSE_RES_ACT)
+    return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_RES_ACT>
+               : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_RES_ACT>;
+  return psb ? dense_kernel<FA, FB, SMODE, false, false, true, FUSE_RES>
+             : dense_kernel<FA, FB, SMODE, false, false, false, FUSE_RES>;
+}
+
 // k_dense_mx4.hip / k_dense_mx5.hip: MX FP8 with A in E4M3 / E5M2.
 dense_fn pick_dense_mx_a4(int eb, int layout, bool psb, int fuse);
 dense_fn pick_dense_mx_a5(int eb, int layout, bool psb, int fuse);
@@ -45,8 +52,18 @@ dense_fn pick_dense_tw_a4(int eb, int layout, bool psb, int fuse);
 dense_fn pick_dense_tw_a5(int eb, int layout, bool psb, int fuse);
 // k_dense_fp4.hip: MXFP4.
 dense_fn pick_dense_fp4(int layout, bool psb, int fuse);
+// k_res_mx4.hip, k_res_mx5.hip, k_res_tw4.hip, k_res_tw5.hip, k_res_fp4.hip:
+// the residual epilogue of each.
+dense_fn pick_residual_mx_a4(int eb, bool psb, int fuse);
+dense_fn pick_residual_mx_a5(int eb, bool psb, int fuse);
+dense_fn pick_residual_tw_a4(int eb, bool psb, int fuse);
+dense_fn pick_residual_tw_a5(int eb, bool psb, int fuse);
+dense_fn pick_residual_fp4(bool psb, int fuse);
 // k_small.hip: the 64 x 64 NT kernel, every format.
 dense_fn pick_small(int ea, int eb, bool mx, bool psb, int fuse);
+// k_rows.hip: 16 fm x 16 (fm 1) or 32 columns with K split over waves, fm 1, 2
+// or 4, residual epilogue.
+dense_fn pick_rows(int ea, int eb, bool mx, bool psb, int fm);
 // k_grouped.hip: the grouped kernels (256 x 256 dense pipeline; persistent
 // streaming with BM-row tiles; the streaming kernel on the dense pipeline's
 // tail pieces).

@@ -42,7 +42,7 @@ EXPORTS = (
     "grouped_int8_gemm_run", "grouped_int8_gemm_validate", "grouped_int8_gemm_variant", "mxgemm_quantize_int8",
     "moe_route_workspace_bytes", "moe_route", "moe_route_backward", "moe_combine", "moe_combine_backward",
     "moe_experts_workspace_bytes", "moe_experts", "moe_experts_validate",
-    "mxgemm_run_residual", "mxgemm_validate_residual", "mxgemm_residual_backward_workspace_bytes",
+    "mxgemm_run_residual", "mxgemm_validate_residual", "mxgemm_residual_variant", "mxgemm_residual_backward_workspace_bytes",
     "mxgemm_residual_backward", "mxgemm_residual_backward_validate",
 )
 
@@ -139,6 +139,8 @@ _lib.mxgemm_run_residual.restype = _i
 _lib.mxgemm_run_residual.argtypes = [_i, _i, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i, _p, _p, _p]
 _lib.mxgemm_validate_residual.restype = _i
 _lib.mxgemm_validate_residual.argtypes = [_i, _i, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i, _p, _p]
+_lib.mxgemm_residual_variant.restype = _i
+_lib.mxgemm_residual_variant.argtypes = [_i, _i, _i, _i64, _i64, _i64]
 _lib.mxgemm_residual_backward_workspace_bytes.restype = _i64
 _lib.mxgemm_residual_backward_workspace_bytes.argtypes = [_i64, _i64]
 _lib.mxgemm_residual_backward.restype = _i
@@ -465,6 +467,12 @@ def validate_residual(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias=None, a
                       z=None):
     return _lib.mxgemm_validate_residual(fmtA, fmtB, layout, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(D), M, N, K,
                                          _ptr(bias), activation, _ptr(residual), _ptr(z))
+
+
+def residual_variant(fmtA, fmtB, layout, M, N, K):
+    """DENSE_TILE256, DENSE_TILE64 or DENSE_ROWS (INT8 also DENSE_TILE128):
+    the kernel run_residual launches for these shapes on the current device."""
+    return _lib.mxgemm_residual_variant(fmtA, fmtB, layout, M, N, K)
 
 
 def residual_backward_workspace_bytes(M, N):

@@ -736,8 +736,8 @@ int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float
  * With neither it is mxgemm_run_fused.  K = 0: z = bias.  Sums may be formed
  * in another order than mxgemm_run's (few rows split K over waves), so the two
  * can differ in the last bit.
- * Errors as mxgemm_run_fused; z the same pointer as D or residual is
- * MXG_ERR_INVALID_ARG.
+ * Errors as mxgemm_run_fused; N above 4194304 is MXG_ERR_UNSUPPORTED, z the
+ * same pointer as D or residual MXG_ERR_INVALID_ARG.
  *
  * mxgemm_residual_backward -- the epilogue's gradient: from dD (D's gradient,
  * which is the residual's too)
@@ -763,6 +763,9 @@ int mxgemm_run_residual(int fmtA, int fmtB, int layout, const void *A, const voi
 int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B,
                              const void *sB, const void *D, int64_t M, int64_t N, int64_t K, const void *bias,
                              int activation, const void *residual, const void *z);
+/* MXG_DENSE_*: the kernel mxgemm_run_residual launches for these sizes on the
+ * current device where it has a residual or z. */
+int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K);
 int64_t mxgemm_residual_backward_workspace_bytes(int64_t M, int64_t N);
 int mxgemm_residual_backward(int activation, const void *dD, const void *z, void *dz, float *dbias, int64_t M,
                              int64_t N, void *workspace, int64_t workspace_bytes, hipStream_t stream);
