@@ -1,62 +1,75 @@
 // The experts of a mixture-of-experts layer for a few tokens, in two kernels:
 //   out[t] = R[t] + sum_e share[t,e] W2[e] act( W1[e] x[t] ),
 //   share[t,e] = sum of w[t,j] over the slots j with ids[t,j] = e.
-// Few tokens make this a stream of the chosen experts' weights: each is read
-// once, 128 bytes of K of 16 rows at a time straight into the matrix cores'
-// layout, and turned into BF16 there (codes of every format are exact in
-// BF16, and so are codes times a power of two inside its range), so that the
-// activations stay what they are: x in BF16, sums in FP32.  act's result h is
-// kept as two BF16 (its rounding and what that leaves, 16 bits of
-// mantissa): rounded to one, it would add as much error as the rounding of
-// out; the second costs a second matrix instruction, which the stream hides.
+// Few tokens make this a stream of the chosen experts' weights: each comes from
+// memory once, in units of 128 bytes of K, and is turned into BF16 in
+// registers (codes of every format are exact in BF16, and so are codes times a
+// power of two inside its range), so that the activations stay what they are: x
+// in BF16, sums in FP32.  act's result h is kept as two BF16 (its rounding
+// and the rounding of what that leaves, 16 bits of mantissa): rounded to one, it
+// would add as much error as the rounding of out (2.3e-3 instead of 1.7e-3 of
+// the result's norm); the second costs a matrix instruction, which the stream hides.
 //
-// experts_up_kernel: a workgroup per (live expert, tile of W1's rows), its
-// waves splitting K; one more workgroup writes the table of live experts and
-// their tokens for experts_down_kernel: a workgroup per tile of out's
-// columns, its waves taking (live expert, part of K) in turn, each adding
-// share * y to sums of its own in LDS; these meet in a fixed order, so a
-// call's bits do not change from run to run.
+// Tokens of an expert beyond 16 make further records of up to 16 of it.
+// experts_up_kernel: a workgroup per (record, tile of W1's rows); one more
+// writes the records and their tokens for experts_down_kernel: a workgroup per
+// tile of out's columns (and split of the records), which walks the records'
+// units of K as one list and adds share * y to sums in LDS when a record ends.
+// No sum's order depends on timing.
+//
+// Two ways of sharing the work of a workgroup's four waves:
+//   private (one or two tokens): 16 rows of the weight, K (down: the list) split
+//     over the waves, each with its own ring of stages; they meet at the end.
+//   shared: 64 rows, 16 per wave, one ring; the activations of a stage, up to 16
+//     rows of them, are brought once for all four waves.
 #pragma once
-#include "common.hpp"
+#include "small.hpp"
 
 namespace mxg {
 
 enum : int { WF_INT8 = 0, WF_BF16 = 1, WF_E4M3 = 2, WF_E5M2 = 3, WF_E2M1 = 4, WF_BLOCK = 5 };
 constexpr int EXP_MAX_T = 64, EXP_MAX_E = 1024, EXP_MAX_TOPK = 32;
+constexpr int EXP_ROWS = 16;                   // tokens of a record
+constexpr int EXP_WAVES = 4;
+constexpr int EXP_SPLIT_BLOCKS = 512;          // workgroups of the second kernel that splits of the list may make
 
 struct ExpertRec {
-  int32_t e, base, n, pad;               // expert, its first pair, its tokens
+  int32_t e, base, n, pad;                     // expert, its first pair, its tokens (1 .. 16)
 };
 struct ExpertPair {
-  int32_t t, row;                        // token, row of h
+  int32_t t;
   float share;
-  int32_t pad;
 };
 
 struct ExpertsArgs {
-  const uint16_t *x;                     // [T, D]
-  const int32_t *ids;                    // [T, topk]
-  const float *w;                        // [T, topk]
+  const uint16_t *x;                           // [T, D]
+  const int32_t *ids;                          // [T, topk]
+  const float *w;                              // [T, topk]
   const uint8_t *w1, *w2;
   const void *s1, *s2;
-  const uint16_t *residual;              // [T, D] or null
-  uint16_t *out;                         // [T, D]
-  uint16_t *h;                           // [2][T topk, F]: high parts, low parts
-  int32_t *live;                         // number of live experts
-  ExpertRec *rec;                        // [live]
-  ExpertPair *pair;                      // [<= T topk], by expert, then by token
-  int64_t D, F, N1;                      // N1 rows of W1[e]: F or 2 F
+  const uint16_t *residual;                    // [T, D] or null
+  uint16_t *out;                               // [T, D]
+  uint16_t *h;                                 // [2][T topk, F]: high parts, low parts, by pair
+  int32_t *count;                              // number of records
+  int32_t *arrived;                            // [tiles of the second kernel]: splits that are done
+  ExpertRec *rec;                              // [records]
+  ExpertPair *pair;                            // [<= T topk], by expert, then by token
+  float *part;                                 // [splits][T][D]: sums of the list's splits
+  int64_t D, F, N1;                            // N1 rows of W1[e]: F or 2 F
   int T, E, topk, act;
-  int tiles, parts;                      // row tiles of W1 (up), parts of K per expert (down)
+  int up_tiles, down_tiles, splits;
 };
 
 // What 16 bytes of a row hold.
 template <int WF> struct WeightFormat {
   static constexpr int CODES = WF == WF_BF16 ? 8 : WF == WF_E2M1 ? 32 : 16;   // values in 16 bytes
   static constexpr int UNIT = 8 * CODES;                                      // values in a 128-byte unit
-  static constexpr int XL = CODES / 4;                                        // 16-byte pieces of x per lane and unit
+  static constexpr int XPITCH = 2 * UNIT;                                     // bytes of an activation row's unit
+  static constexpr int SUB = CODES / 8;                                       // matrix instructions per 16 bytes
   static constexpr bool MX = WF == WF_E4M3 || WF == WF_E5M2 || WF == WF_E2M1;
-  static constexpr int SCALES = WF == WF_E2M1 ? 2 : 1;                        // E8M0 scales per lane and unit
+  // tokens up to which the waves work apart: what one DMA brings of them, in
+  // two planes
+  static constexpr int PRIVATE_T = WF == WF_E2M1 ? 1 : 2;
   __host__ __device__ static int64_t row_bytes(int64_t K) { return K * 16 / CODES; }
 };
 
@@ -91,119 +104,179 @@ __device__ inline bf16x8_t weight_values(const v4i &raw, int m, float scale) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
-// acc[m][b] += rows 16 b .. of a weight tile times the activation rows xo[m]
-// (byte offsets into rx, NOWHERE: none), over the 128-byte units u0, u0 + du,
-// .. below u1 of K.  Lane (i = lane % 16, q = lane / 16) holds bytes 32 q .. +
-// 31 of a unit of weight row i and the same values of activation row i;
-// the result lane holds weight rows 4 q .. + 3 of activation row i.  PL planes of
-// activations (plane bytes apart) are summed.  Loads run U units ahead.
-constexpr uint32_t EXP_NOWHERE = 0x80000000u;   // past any resource: zeros, no memory read
+// A wave's stream of stages through a ring in LDS.  A stage is one 128-byte
+// unit of K of the wave's 16 weight rows, with its scales, and the same
+// values of up to RC activation rows in PL planes (private: as many as make
+// 1 KiB, one DMA); DOWN: the record's pairs too.
+// All of it comes by DMA (nothing in registers while it is in flight), a
+// constant number of DMAs per stage, so that the counter of outstanding ones tells
+// which stages have landed: stages that do not exist are asked for past the end
+// of their resources, which writes zeros and reads no memory.
+//
+// LDS of a stage: [W: 4 x 2 KiB][X: PL planes][S: 4 x 256 B][pairs: 4 x 128 B],
+// a quarter of W, S and the pairs per wave; X a quarter per wave (private) or
+// whole (shared).
+//   W: row r of 128 bytes, 16-byte piece p at position p ^ kswz(r); lane (i, q)
+//     of a matrix instruction takes pieces q and q + 4 of row i.
+//   X: rows of XPITCH bytes, piece p at position p ^ xswz(r): the values beside
+//     weight piece p are pieces SUB p ..; each read's 16-lane phases (see kswz)
+//     land on 16 different 16-byte bank groups: rows {0-3, 12-15} at one value of
+//     q and {4-11} at the next, so the set of xswz of the first eight must not change
+//     when it is shifted by the XOR of their pieces (1, 2 or 4).
+//   S: the aligned dwords around a row's E8M0 scales of the unit (2 per row,
+//     E2M1 4); the channel scales (INT8, DOWN); the unit's block scale.
+template <int WF, int PL, bool SHARED, bool DOWN, int U>
+struct ExpertStream {
+  typedef WeightFormat<WF> F;
+  static constexpr int RC = SHARED ? EXP_ROWS : F::PRIVATE_T;
+  // shared: XI DMAs per wave and plane, a plane after the other; private: one
+  // DMA, RC rows of each plane
+  static constexpr int XI = SHARED ? (RC * F::XPITCH / EXP_WAVES + 1023) / 1024 : 1;
+  static constexpr int XD = SHARED ? PL * XI : 1;                                       // DMAs per wave
+  static constexpr int XPLANE = SHARED ? EXP_WAVES * XI * 1024 : RC * F::XPITCH;
+  static constexpr int XSIZE = SHARED ? PL * XPLANE : EXP_WAVES * 1024;
+  static_assert(SHARED || PL * RC * F::XPITCH <= 1024, "one DMA");
+  static constexpr bool S = F::MX || WF == WF_BLOCK || (DOWN && WF == WF_INT8);
+  static constexpr int W_OFF = 0, X_OFF = EXP_WAVES * 2048;
+  static constexpr int S_OFF = X_OFF + XSIZE;
+  static constexpr int P_OFF = S_OFF + (S ? EXP_WAVES * 256 : 0);
+  static constexpr int STAGE = P_OFF + (DOWN ? EXP_WAVES * 256 : 0);
+  static constexpr int LDS_BYTES = U * STAGE;
+  static constexpr int DMAS = 2 + XD + (S ? 1 : 0) + (DOWN ? 1 : 0);
+  static_assert((U - 1) * DMAS < 64, "vmcnt is 6 bits");
 
-template <int WF, int FM, int FN, int PL, int U>
-__device__ inline void stream_product(__amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rx,
-                                      const uint32_t (&xo)[FM], uint32_t plane, int64_t K, int u0, int u1, int du,
-                                      v4f (&acc)[FM][FN]) {
-  typedef WeightFormat<WF> W;
-  const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
-  const uint32_t KB = (uint32_t)W::row_bytes(K), SK = (uint32_t)(K / 32);
-  const uint32_t wo = (uint32_t)i16 * KB + 32u * q;
-  v4i w[U][FN][2], x[U][FM][PL][W::XL];
-  uint32_t sc[U][FN][W::SCALES];
-  float blk[U];
-  auto load = [&](int s, int u) {
-    const bool in0 = 128u * u + 32u * q < KB, in1 = 128u * u + 32u * q + 16u < KB;
+  __device__ static inline int xswz(int r) {
+    if constexpr (WF == WF_BF16) return kswz(r);
+    else if constexpr (WF == WF_E2M1) return (r & 3) ^ (r & 4 ? 12 : 0) ^ (r & 8);
+    else return r;
+  }
+
+  int lane, w, i16, q;
+  uint32_t lds0;
+  uint32_t KB, K, SK, units;
+  uint32_t vo, vo_tail;                        // weight rows: lane offsets; in the last unit
+  uint32_t xv[XI], xv_tail[XI];                // activation rows
+  uint32_t xplane;                             // bytes between planes in memory
+  u32x4 rw, rs, rx, rp;
+  uint32_t pair0;                              // byte offset of the record's pairs
+
+  __device__ inline void init(uint8_t *smem, int64_t K_, u32x4 rx_, uint32_t xplane_) {
+    lane = threadIdx.x & 63;
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    i16 = lane & 15;
+    q = lane >> 4;
+    lds0 = lds_addr(smem);
+    K = (uint32_t)K_;
+    KB = (uint32_t)F::row_bytes(K_);
+    SK = K / 32;
+    units = (KB + 127) / 128;
+    const int r8 = lane >> 3, piece = (lane & 7) ^ kswz(r8);
+    vo = (uint32_t)r8 * KB + 16u * piece;
+    vo_tail = 128u * (units - 1) + 16u * piece < KB ? vo : NOWHERE;
+    rx = rx_;
+    xplane = xplane_;
+    rw = rs = rp = rsrc4(smem, 0);             // until the first record: nothing
+    pair0 = 0;
 #pragma unroll
-    for (int b = 0; b < FN; ++b) {
-      const uint32_t o = wo + 16u * b * KB + 128u * u;
-      w[s][b][0] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(in0 ? o : EXP_NOWHERE), 0, 0));
-      w[s][b][1] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(in1 ? o + 16u : EXP_NOWHERE), 0, 0));
-      if constexpr (W::MX) {
-        // a lane's 32 (E2M1: 64) values: one E8M0 scale (two)
-        const uint32_t so = (16u * b + i16) * SK + (uint32_t)(u * (W::UNIT / 32)) + W::SCALES * q;
-        sc[s][b][0] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(in0 ? so : EXP_NOWHERE), 0, 0);
-        if constexpr (W::SCALES == 2) sc[s][b][1] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(in1 ? so + 1u : EXP_NOWHERE), 0, 0);
-      }
-    }
-    if constexpr (WF == WF_BLOCK) blk[s] = __uint_as_float(buf_load_u32(rs, 4u * u));
+    for (int k = 0; k < XI; ++k) xv[k] = xv_tail[k] = NOWHERE;
+  }
+  static constexpr uint32_t NOWHERE = 0x80000000u;
+
+  // The wave's weight rows: n0 .. n0 + 15 of [N, K] of expert e, and their scales.
+  __device__ inline void set_weight(const uint8_t *wt, const void *s, int64_t e, int64_t N, int64_t n0) {
+    rw = rsrc4(wt + (e * N + n0) * KB, clamp_records((N - n0) * KB));
+    if constexpr (F::MX) rs = rsrc4((const uint8_t *)s + (e * N + n0) * SK, clamp_records((N - n0) * SK));
+    else if constexpr (WF == WF_BLOCK)
+      rs = rsrc4((const float *)s + (e * (N / 128) + n0 / 128) * (K / 128), n0 < N ? 4 * (K / 128) : 0u);
+    else if constexpr (S) rs = rsrc4((const float *)s + e * N + n0, clamp_records(4 * (N - n0)));
+  }
+
+  // The activation rows: row_at(r) is row r's byte offset, r < n.
+  template <class RowAt>
+  __device__ inline void set_rows(int n, RowAt row_at) {
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
-#pragma unroll
-      for (int p = 0; p < PL; ++p)
-#pragma unroll
-        for (int j = 0; j < W::XL; ++j) {
-          const bool in = xo[m] != EXP_NOWHERE && (j < W::XL / 2 ? in0 : in1);
-          const uint32_t o = xo[m] + p * plane + 2u * (uint32_t)(u * W::UNIT + q * 2 * W::CODES) + 16u * j;
-          x[s][m][p][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? o : EXP_NOWHERE), 0, 0));
-        }
-  };
-#pragma unroll
-  for (int s = 0; s < U; ++s)
-    if (u0 + s * du < u1) load(s, u0 + s * du);
-  for (int u = u0; u < u1; u += U * du) {
-#pragma unroll
-    for (int s = 0; s < U; ++s) {
-      if (u + s * du < u1) {
-        v4f part[FM][FN];
-        if constexpr (WF == WF_BLOCK) {
-#pragma unroll
-          for (int m = 0; m < FM; ++m)
-#pragma unroll
-            for (int b = 0; b < FN; ++b) part[m][b] = (v4f){0.f, 0.f, 0.f, 0.f};
-        }
-#pragma unroll
-        for (int j = 0; j < W::XL; ++j)
-#pragma unroll
-          for (int b = 0; b < FN; ++b) {
-            constexpr int HALF = W::XL / 2;
-            float scale = 1.0f;
-            if constexpr (W::MX) scale = __uint_as_float(sc[s][b][W::SCALES == 2 ? j / HALF : 0] << 23);
-            const bf16x8_t wv = weight_values<WF>(w[s][b][j / HALF], j % HALF, scale);
-#pragma unroll
-            for (int m = 0; m < FM; ++m)
-#pragma unroll
-              for (int p = 0; p < PL; ++p) {
-                v4f &c = WF == WF_BLOCK ? part[m][b] : acc[m][b];
-                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, x[s][m][p][j]), c, 0, 0, 0);
-              }
-          }
-        if constexpr (WF == WF_BLOCK) {
-          // one FP32 scale for 128 values of K of all of the tile's rows
-#pragma unroll
-          for (int m = 0; m < FM; ++m)
-#pragma unroll
-            for (int b = 0; b < FN; ++b) acc[m][b] += part[m][b] * blk[s];
-        }
-        if (u + (s + U) * du < u1) load(s, u + (s + U) * du);
-      }
+    for (int k = 0; k < XI; ++k) {
+      const int at = ((SHARED ? w * XI : 0) + k) * 1024 + 16 * lane;
+      const int row = at / F::XPITCH, pl = SHARED ? 0 : row / RC, r = SHARED ? row : row % RC;
+      const int piece = (at % F::XPITCH / 16) ^ xswz(r);
+      xv[k] = r < n && pl < PL ? row_at(r) + pl * xplane + 16u * piece : NOWHERE;
+      xv_tail[k] = (units - 1) * F::UNIT + 8u * piece < K ? xv[k] : NOWHERE;
     }
   }
-}
 
-// Resources of rows n0 .. of a weight [N, K] (N rows in all, of expert e) and
-// of their scales; past the last row everything reads zero.
-template <int WF>
-__device__ inline void weight_rsrc(const uint8_t *w, const void *s, int64_t e, int64_t N, int64_t K, int64_t n0,
-                                   __amdgpu_buffer_rsrc_t &rw, __amdgpu_buffer_rsrc_t &rs) {
-  const int64_t KB = WeightFormat<WF>::row_bytes(K);
-  rw = make_rsrc(w + (e * N + n0) * KB, clamp_records((N - n0) * KB));
-  if constexpr (WeightFormat<WF>::MX)
-    rs = make_rsrc((const uint8_t *)s + (e * N + n0) * (K / 32), clamp_records((N - n0) * (K / 32)));
-  else if constexpr (WF == WF_BLOCK)
-    rs = make_rsrc((const float *)s + (e * (N / 128) + n0 / 128) * (K / 128), clamp_records(4 * (K / 128)));
-  else
-    rs = make_rsrc(w, 0);
-}
-
-// The channel scales of rows n0 + c .. + 3 (INT8; else 1).
-template <int WF>
-__device__ inline v4f channel_scales(const void *s, int64_t e, int64_t N, int64_t n0, int c) {
-  if constexpr (WF == WF_INT8) {
-    const __amdgpu_buffer_rsrc_t r = make_rsrc((const float *)s + e * N + n0, clamp_records(4 * (N - n0)));
-    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * c, 0, 0));
-  } else {
-    return (v4f){1.f, 1.f, 1.f, 1.f};
+  // Unit u (live: it exists) into ring slot sl.
+  __device__ inline void issue(int sl, uint32_t u, bool live) {
+    const uint32_t st = lds0 + (uint32_t)sl * STAGE;
+    const bool last = u + 1 == units;
+    const uint32_t vw = !live ? NOWHERE : last ? vo_tail : vo;
+    const uint32_t wd = st + W_OFF + 2048u * w;
+    dma_asm_v<16, 0>(wd, rw, vw, live ? 128u * u : 0u);
+    dma_asm_v<16, 1024>(wd, rw, vw, live ? 128u * u + 8u * KB : 0u);
+    const uint32_t xd = st + X_OFF + (SHARED ? (uint32_t)w * XI * 1024u : (uint32_t)w * 1024u);
+    static_for<0, SHARED ? PL : 1>([&](auto pc) {
+      static_for<0, XI>([&](auto kc) {
+        constexpr int p = decltype(pc)::value, k = decltype(kc)::value;
+        const uint32_t v = !live ? NOWHERE : last ? xv_tail[k] : xv[k];
+        dma_asm_v<16, p * XPLANE + k * 1024>(xd, rx, v, live ? u * F::XPITCH + p * xplane : 0u);
+      });
+    });
+    if constexpr (S) {
+      uint32_t v = NOWHERE;
+      if constexpr (WF == WF_E2M1) v = (((uint32_t)(lane >> 2) * SK + 8u * u) & ~3u) + 4u * (lane & 3);
+      else if constexpr (F::MX) v = lane < 32 ? (((uint32_t)(lane >> 1) * SK + 4u * u) & ~3u) + 4u * (lane & 1) : NOWHERE;
+      else if constexpr (WF == WF_BLOCK) v = lane == 0 ? 4u * u : NOWHERE;
+      else v = lane < 16 ? 4u * lane : NOWHERE;
+      dma_asm_v<4>(st + S_OFF + 256u * w, rs, live ? v : NOWHERE, 0u);
+    }
+    if constexpr (DOWN)
+      dma_asm_v<4>(st + P_OFF + 256u * w, rp, live && lane < 32 ? 4u * lane : NOWHERE, live ? pair0 : 0u);
   }
-}
+
+  // Stage v has landed once at most the later stages' DMAs are outstanding
+  // (U - 2 of them are in flight); the reads of the stage before it are done.
+  __device__ static inline void wait() {
+    constexpr int N = (U - 2) * DMAS;
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+    if constexpr (SHARED) __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // acc += the stage's product: the result lane holds weight rows 4 q .. + 3 of
+  // activation row i.
+  __device__ inline void consume(const uint8_t *smem, int sl, uint32_t u, v4f &acc) const {
+    const uint8_t *st = smem + sl * STAGE;
+    const uint8_t *wt = st + W_OFF + 2048 * w + i16 * 128;
+    const int ri = i16 & (RC - 1), f = xswz(ri);
+    const uint8_t *xt = st + X_OFF + (SHARED ? 0 : w * 1024) + ri * F::XPITCH;
+    const uint8_t *sc = st + S_OFF + 256 * w;
+    const v4i raw[2] = {lds_read16(wt + ((q ^ kswz(i16)) << 4)), lds_read16(wt + (((q + 4) ^ kswz(i16)) << 4))};
+    v4f part = WF == WF_BLOCK ? (v4f){0.f, 0.f, 0.f, 0.f} : acc;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int piece = q + 4 * h;
+      float scale = 1.0f;
+      if constexpr (F::MX) {
+        const uint32_t skew = ((uint32_t)i16 * SK + u * (F::UNIT / 32)) & 3u;
+        const int at = WF == WF_E2M1 ? i16 * 16 + piece : i16 * 8 + (piece >> 1);
+        // past K the codes are zero and the byte is not this row's
+        if (128u * u + 16u * piece < KB) scale = __uint_as_float((uint32_t)sc[at + skew] << 23);
+      }
+#pragma unroll
+      for (int m = 0; m < F::SUB; ++m) {
+        const bf16x8_t wv = weight_values<WF>(raw[h], m, scale);
+#pragma unroll
+        for (int p = 0; p < PL; ++p) {
+          const v4i xr = lds_read16(xt + p * XPLANE + (((piece * F::SUB + m) ^ f) << 4));
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, xr), part, 0, 0, 0);
+        }
+      }
+    }
+    // one FP32 scale for 128 values of K of all of the tile's rows
+    if constexpr (WF == WF_BLOCK) acc += part * *(const float *)sc;
+    else acc = part;
+  }
+};
 
 // The tokens of every expert as bits.
 struct ExpertMasks {
@@ -224,77 +297,94 @@ __device__ inline uint64_t expert_mask(const ExpertMasks &mk, int e) {
   return (uint64_t)mk.bits[e][1] << 32 | mk.bits[e][0];
 }
 
-// The live expert of this rank (by index), or -1; every wave for itself.
-__device__ inline int live_expert(const ExpertsArgs &p, const ExpertMasks &mk, int rank) {
+// For 64 experts, one per lane: their tokens n, and before each of them the
+// records (16 tokens or fewer each) and the pairs, of these 64.
+__device__ inline void expert_scan(const ExpertsArgs &p, const ExpertMasks &mk, int e, int &n, int &recs, int &pairs,
+                                   int &all_recs, int &all_pairs) {
   const int lane = threadIdx.x & 63;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    const bool on = e0 + lane < p.E && expert_mask(mk, e0 + lane) != 0;
-    const uint64_t b = __ballot(on);
-    const int n = __popcll(b);
-    if (rank < n) {
-      const uint64_t me = __ballot(on && __popcll(b & ((1ull << lane) - 1)) == rank);
-      return e0 + __ffsll((unsigned long long)me) - 1;
-    }
-    rank -= n;
+  n = e < p.E ? __popcll(expert_mask(mk, e)) : 0;
+  const int mine = (n + EXP_ROWS - 1) / EXP_ROWS << 16 | n;     // both counts stay below 2^12
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
   }
-  return -1;
+  const int all = __shfl(sum, 63);
+  recs = (sum - mine) >> 16;
+  pairs = (sum - mine) & 0xFFFF;
+  all_recs = all >> 16;
+  all_pairs = all & 0xFFFF;
 }
 
-// The slot of token t that first names expert e.
-__device__ inline int first_slot(const ExpertsArgs &p, int t, int e) {
-  int j = 0;
-  while (j < p.topk - 1 && p.ids[t * p.topk + j] != e) ++j;
-  return j;
+// Record `rank` and its tokens as bits (n = 0: there is none); every wave for itself.
+__device__ inline ExpertRec find_record(const ExpertsArgs &p, const ExpertMasks &mk, int rank, uint64_t &tokens) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int n, recs, pairs, all_recs, all_pairs;
+    expert_scan(p, mk, e0 + lane, n, recs, pairs, all_recs, all_pairs);
+    if (rank < all_recs) {
+      const uint64_t me = __ballot(n > 0 && recs <= rank && rank < recs + (n + EXP_ROWS - 1) / EXP_ROWS);
+      const int l = __ffsll((unsigned long long)me) - 1;
+      const int skip = EXP_ROWS * (rank - __shfl(recs, l));
+      tokens = expert_mask(mk, e0 + l);
+      for (int k = 0; k < skip; ++k) tokens &= tokens - 1;
+      const int left = __shfl(n, l) - skip;
+      return ExpertRec{e0 + l, base + __shfl(pairs, l) + skip, left < EXP_ROWS ? left : EXP_ROWS, 0};
+    }
+    rank -= all_recs;
+    base += all_pairs;
+  }
+  tokens = 0;
+  return ExpertRec{0, 0, 0, 0};
 }
 
-// The table for the second kernel, by one workgroup.
+// The tables for the second kernel, by one workgroup.
 __device__ inline void expert_table(const ExpertsArgs &p, const ExpertMasks &mk, int32_t (&first)[EXP_MAX_E]) {
   const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x; i < p.down_tiles; i += blockDim.x)
+    if (p.splits > 1) p.arrived[i] = 0;
   if (threadIdx.x < 64) {
-    int live = 0, base = 0;
+    int rec0 = 0, pair0 = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int n = e < p.E ? __popcll(expert_mask(mk, e)) : 0;
-      int sum = n;                         // of the lanes up to this one
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(sum, d);
-        if (lane >= d) sum += o;
-      }
-      const uint64_t b = __ballot(n > 0);
-      if (e < p.E) first[e] = base + sum - n;
-      if (n > 0) p.rec[live + __popcll(b & ((1ull << lane) - 1))] = ExpertRec{e, base + sum - n, n, 0};
-      live += __popcll(b);
-      base += __shfl(sum, 63);
+      int n, recs, pairs, all_recs, all_pairs;
+      expert_scan(p, mk, e0 + lane, n, recs, pairs, all_recs, all_pairs);
+      if (e0 + lane < p.E) first[e0 + lane] = pair0 + pairs;
+      for (int k = 0; k < n; k += EXP_ROWS)
+        p.rec[rec0 + recs + k / EXP_ROWS] =
+            ExpertRec{e0 + lane, pair0 + pairs + k, n - k < EXP_ROWS ? n - k : EXP_ROWS, 0};
+      rec0 += all_recs;
+      pair0 += all_pairs;
     }
-    if (lane == 0) *p.live = live;
+    if (lane == 0) *p.count = rec0;
   }
   __syncthreads();
   for (int s = threadIdx.x; s < p.T * p.topk; s += blockDim.x) {
-    const int e = p.ids[s], t = s / p.topk;
-    if (e < 0 || e >= p.E || s != t * p.topk + first_slot(p, t, e)) continue;
+    const int e = p.ids[s], t = s / p.topk, j0 = s - t * p.topk;
+    if (e < 0 || e >= p.E) continue;
     float share = 0.0f;
-    for (int j = s - t * p.topk; j < p.topk; ++j)
-      if (p.ids[t * p.topk + j] == e) share += p.w[t * p.topk + j];
-    p.pair[first[e] + __popcll(expert_mask(mk, e) & ((1ull << t) - 1))] = ExpertPair{t, s, share, 0};
+    bool again = false;                        // the token named this expert before
+    for (int j = 0; j < p.topk; ++j) {
+      if (p.ids[t * p.topk + j] != e) continue;
+      again |= j < j0;
+      share += p.w[t * p.topk + j];
+    }
+    if (!again) p.pair[first[e] + __popcll(expert_mask(mk, e) & ((1ull << t) - 1))] = ExpertPair{t, share};
   }
 }
 
 // h of four consecutive rows of W1 (two SwiGLU pairs), as two BF16 each.
 __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v4f &z) {
   const int64_t plane = (int64_t)p.T * p.topk * p.F;
-  v4f v;
-  int cnt = 4;
-  int64_t c = n;
-  if (p.act == ACT_SWIGLU) {
+  const bool gated = p.act == ACT_SWIGLU;
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (gated) {
     v.x = z.x * logistic_f32(z.x) * z.y;
     v.y = z.z * logistic_f32(z.z) * z.w;
-    v.z = v.w = 0.0f;
-    cnt = 2;
-    c = n >> 1;
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = activate(p.act, z[k]);
+    for (int k = 0; k < 4; ++k) v[k] = activate_select(p.act, z[k]);
   }
   const uint32_t hi[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
   float r[4];
@@ -305,8 +395,8 @@ __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v
     r[k] = fabsf(f) < __builtin_inff() ? v[k] - f : 0.0f;
   }
   const uint32_t lo[2] = {pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
-  uint16_t *dst = p.h + (int64_t)row * p.F + c;
-  if (cnt == 2) {
+  uint16_t *dst = p.h + (int64_t)row * p.F + (gated ? n >> 1 : n);
+  if (gated) {
     *(uint32_t *)dst = hi[0];
     *(uint32_t *)(dst + plane) = lo[0];
   } else {
@@ -315,140 +405,200 @@ __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v
   }
 }
 
-constexpr int UP_WAVES = 4, UP_FN = 2;
-
-template <int WF, int FMAX>
-__global__ __launch_bounds__(64 * UP_WAVES) void experts_up_kernel(ExpertsArgs p) {
-  constexpr int FN = UP_FN, W = UP_WAVES;
-  __shared__ union {
+template <int WF, bool SHARED>
+__global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs p) {
+  constexpr int U = SHARED ? 4 : 6, ROWS = SHARED ? 16 * EXP_WAVES : 16;
+  typedef ExpertStream<WF, 1, SHARED, false, U> Stream;
+  __shared__ __attribute__((aligned(1024))) union {
     struct {
       ExpertMasks mk;
       int32_t first[EXP_MAX_E];
     } t;
-    v4f part[W][FMAX * FN][64];
+    uint8_t ring[Stream::LDS_BYTES];
+    v4f part[EXP_WAVES][64];
   } sm;
-  __shared__ int32_t row[EXP_MAX_T], tok[EXP_MAX_T];
-  const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ int32_t tok[EXP_ROWS];
   expert_masks(p, sm.t.mk);
   if (blockIdx.x == 0) {
     expert_table(p, sm.t.mk, sm.t.first);
     return;
   }
-  const int rank = (int)(blockIdx.x - 1) / p.tiles, tile = (int)(blockIdx.x - 1) - rank * p.tiles;
-  const int e = __builtin_amdgcn_readfirstlane(live_expert(p, sm.t.mk, rank));
-  if (e < 0) return;
-  const uint64_t mask = expert_mask(sm.t.mk, e);
-  const int n = __popcll(mask);
-  if (w == 0 && (mask >> lane & 1)) {
-    const int i = __popcll(mask & ((1ull << lane) - 1));
-    tok[i] = lane;
-    row[i] = lane * p.topk + first_slot(p, lane, e);
-  }
-  __syncthreads();                         // the masks are free from here on
+  const int rank = (int)(blockIdx.x - 1) / p.up_tiles, tile = (int)(blockIdx.x - 1) - rank * p.up_tiles;
+  uint64_t tokens;
+  ExpertRec rec = find_record(p, sm.t.mk, rank, tokens);
+  rec.e = __builtin_amdgcn_readfirstlane(rec.e);
+  rec.n = __builtin_amdgcn_readfirstlane(rec.n);
+  if (rec.n == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int place = __popcll(tokens & ((1ull << lane) - 1));
+  if (threadIdx.x < 64 && (tokens >> lane & 1) && place < EXP_ROWS) tok[place] = lane;
+  __syncthreads();                             // and the masks' memory is free from here on
 
-  const int64_t n0 = (int64_t)tile * (16 * FN);
-  __amdgpu_buffer_rsrc_t rw, rs;
-  weight_rsrc<WF>(p.w1, p.s1, e, p.N1, p.D, n0, rw, rs);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, clamp_records(2 * p.T * p.D));
-  const int units = (int)((WeightFormat<WF>::row_bytes(p.D) + 127) / 128);
-  auto body = [&](auto fc) {
-    constexpr int FM = decltype(fc)::value;
-    constexpr int U = FM == 1 ? 3 : FM == 2 && WF != WF_E2M1 ? 2 : 1;
-    uint32_t xo[FM];
-    v4f acc[FM][FN];
+  Stream s;
+  s.init(sm.ring, p.D, rsrc4(p.x, clamp_records(2 * p.T * p.D)), 0u);
+  const int64_t n0 = (int64_t)tile * ROWS + (SHARED ? 16 * s.w : 0);
+  s.set_weight(p.w1, p.s1, rec.e, p.N1, n0);
+  s.set_rows(rec.n, [&](int r) { return (uint32_t)(2 * tok[r] * p.D); });
+  const int c = 4 * s.q;
+  v4f chan = {1.f, 1.f, 1.f, 1.f};
+  if constexpr (WF == WF_INT8) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc((const float *)p.s1 + rec.e * p.N1 + n0, clamp_records(4 * (p.N1 - n0)));
+    chan = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * c, 0, 0));
+    // here, not among the ring's DMAs
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      xo[m] = 16 * m + i16 < n ? (uint32_t)(2 * tok[16 * m + i16] * p.D) : EXP_NOWHERE;
+    for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(chan[k]));
+  }
+  const int units = (int)s.units;
+  const int lo = SHARED ? 0 : s.w * units / EXP_WAVES, hi = SHARED ? units : (s.w + 1) * units / EXP_WAVES;
 #pragma unroll
-      for (int b = 0; b < FN; ++b) acc[m][b] = (v4f){0.f, 0.f, 0.f, 0.f};
-    }
-    stream_product<WF, FM, FN, 1, U>(rw, rs, rx, xo, 0u, p.D, w, units, W, acc);
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-#pragma unroll
-      for (int b = 0; b < FN; ++b) sm.part[w][m * FN + b][lane] = acc[m][b];
+  for (int k = 0; k < U - 1; ++k) s.issue(k, lo + k, lo + k < hi);
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  int sl = 0;
+  for (int v = lo; v < hi; ++v) {
+    Stream::wait();
+    s.issue(sl == 0 ? U - 1 : sl - 1, v + U - 1, v + U - 1 < hi);
+    s.consume(sm.ring, sl, v, acc);
+    sl = sl == U - 1 ? 0 : sl + 1;
+  }
+  wait_vmem_le<0>();                           // no DMA into LDS that is used for something else
+  if constexpr (!SHARED) {
     __syncthreads();
-    for (int f = w; f < FM * FN; f += W) {
-      const int i = 16 * (f / FN) + i16, c = 16 * (f % FN) + 4 * q;
-      v4f z = sm.part[0][f][lane];
+    sm.part[s.w][s.lane] = acc;
+    __syncthreads();
+    if (s.w != 0) return;
 #pragma unroll
-      for (int k = 1; k < W; ++k) z += sm.part[k][f][lane];
-      if (i < n && n0 + c < p.N1) store_h(p, row[i], n0 + c, z * channel_scales<WF>(p.s1, e, p.N1, n0, c));
-    }
-  };
-  if (FMAX == 1 || n <= 16) body(std::integral_constant<int, 1>{});
-  else if (n <= 32) body(std::integral_constant<int, FMAX == 1 ? 1 : 2>{});
-  else body(std::integral_constant<int, FMAX>{});
+    for (int k = 1; k < EXP_WAVES; ++k) acc += sm.part[k][s.lane];
+  }
+  if (s.i16 < rec.n && n0 + c < p.N1) store_h(p, rec.base + s.i16, n0 + c, acc * chan);
 }
 
-constexpr int DOWN_WAVES = 8, DOWN_FN = 1;
-constexpr int DOWN_PITCH = 16 * DOWN_FN + 4;     // floats per token: columns and a skew
-
-inline __host__ __device__ int down_lds_bytes(int T) { return 4 * DOWN_WAVES * T * DOWN_PITCH; }
-
-template <int WF, int FMAX>
-__global__ __launch_bounds__(64 * DOWN_WAVES) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int FN = DOWN_FN, W = DOWN_WAVES, COLS = 16 * FN;
-  extern __shared__ __attribute__((aligned(16))) float sums[];   // [W][T][DOWN_PITCH]
-  const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float *mine = sums + w * p.T * DOWN_PITCH;
-  for (int i = lane; i < p.T * DOWN_PITCH; i += 64) mine[i] = 0.0f;
-  const int64_t n0 = (int64_t)blockIdx.x * COLS;
-  const int live = __builtin_amdgcn_readfirstlane(*p.live);
-  const int units = (int)((WeightFormat<WF>::row_bytes(p.F) + 127) / 128);
-  const int per = (units + p.parts - 1) / p.parts;
-  const int64_t plane = (int64_t)p.T * p.topk * p.F;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.h, clamp_records(4 * plane));
-  for (int job = w; job < live * p.parts; job += W) {
-    const int a = job / p.parts, part = job - a * p.parts;
-    const int e = __builtin_amdgcn_readfirstlane(p.rec[a].e), base = __builtin_amdgcn_readfirstlane(p.rec[a].base);
-    const int n = __builtin_amdgcn_readfirstlane(p.rec[a].n);
-    __amdgpu_buffer_rsrc_t rw, rs;
-    weight_rsrc<WF>(p.w2, p.s2, e, p.D, p.F, n0, rw, rs);
-    auto body = [&](auto fc) {
-      constexpr int FM = decltype(fc)::value;
-      constexpr int U = FM == 1 ? 2 : 1;
-      uint32_t xo[FM];
-      int t[FM];
-      float share[FM];
-      v4f acc[FM][FN];
-#pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        const bool in = 16 * m + i16 < n;
-        const ExpertPair pr = p.pair[base + (in ? 16 * m + i16 : 0)];
-        xo[m] = in ? (uint32_t)(2 * pr.row * p.F) : EXP_NOWHERE;
-        t[m] = in ? pr.t : -1;
-        share[m] = pr.share;
-#pragma unroll
-        for (int b = 0; b < FN; ++b) acc[m][b] = (v4f){0.f, 0.f, 0.f, 0.f};
-      }
-      stream_product<WF, FM, FN, 2, U>(rw, rs, rx, xo, (uint32_t)(2 * plane), p.F, part * per, min(units, (part + 1) * per), 1, acc);
-#pragma unroll
-      for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int b = 0; b < FN; ++b)
-          if (t[m] >= 0) {
-            const int c = 16 * b + 4 * q;
-            v4f *s = (v4f *)(mine + t[m] * DOWN_PITCH + c);
-            *s += acc[m][b] * channel_scales<WF>(p.s2, e, p.D, n0, c) * share[m];
-          }
-    };
-    if (FMAX == 1 || n <= 16) body(std::integral_constant<int, 1>{});
-    else if (n <= 32) body(std::integral_constant<int, FMAX == 1 ? 1 : 2>{});
-    else body(std::integral_constant<int, FMAX>{});
-  }
+// TM: the most tokens (the sums' rows).
+template <int WF, bool SHARED, int TM>
+__global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArgs p) {
+  constexpr int U = !SHARED ? 5 : TM > 16 ? 3 : 4, COLS = SHARED ? 16 * EXP_WAVES : 16, SETS = SHARED ? 1 : EXP_WAVES;
+  constexpr int PITCH = COLS + 4;              // floats per token: columns and a skew
+  typedef ExpertStream<WF, 2, SHARED, true, U> Stream;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[Stream::LDS_BYTES];
+  __shared__ __attribute__((aligned(16))) float sums[SETS][TM][PITCH];
+  __shared__ int32_t done;
+  for (int i = threadIdx.x; i < SETS * TM * PITCH; i += 64 * EXP_WAVES) (&sums[0][0][0])[i] = 0.0f;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.T * COLS; i += 64 * W) {
-    const int t = i / COLS, c = i - t * COLS;
-    if (n0 + c >= p.D) continue;
-    float v = sums[t * DOWN_PITCH + c];
+  const int tile = (int)blockIdx.x / p.splits, split = (int)blockIdx.x - tile * p.splits;
+  const int64_t tile0 = (int64_t)tile * COLS, plane = (int64_t)p.T * p.topk * p.F;
+  Stream s;
+  s.init(ring, p.F, rsrc4(p.h, clamp_records(4 * plane)), (uint32_t)(2 * plane));
+  const int64_t n0 = tile0 + (SHARED ? 16 * s.w : 0);
+  s.rp = rsrc4(p.pair, (uint32_t)(8 * p.T * p.topk));
+  // read as constants, through the scalar cache: the kernel before wrote them
+  typedef const __attribute__((address_space(4))) ExpertRec *RecPtr;
+  const RecPtr recs = (RecPtr)(uintptr_t)p.rec;
+  const int units = (int)s.units;
+  const int total = __builtin_amdgcn_readfirstlane(*p.count) * units;
+  const int pieces = SHARED ? p.splits : EXP_WAVES, mine = SHARED ? split : s.w;
+  const int lo = (int)((int64_t)total * mine / pieces), hi = (int)((int64_t)total * (mine + 1) / pieces);
+
+  // the stage to issue, and the one to use: record and unit
+  int ia = units > 0 ? lo / units : 0, iu = lo - ia * units;
+  int ca = ia, cu = iu, at = lo;
+  auto enter = [&](int a) {
+    const int e = recs[a].e, base = recs[a].base, n = recs[a].n;
+    s.set_weight(p.w2, p.s2, e, p.D, n0);
+    s.set_rows(n, [&](int r) { return (uint32_t)(2 * (base + r) * p.F); });
+    s.pair0 = 8u * base;
+  };
+  auto issue = [&](int sl) {
+    s.issue(sl, iu, at < hi);
+    ++at;
+    if (++iu == units) {
+      iu = 0;
+      ++ia;
+      if (at < hi) enter(ia);
+    }
+  };
+  if (lo < hi) enter(ia);
 #pragma unroll
-    for (int k = 1; k < W; ++k) v += sums[(k * p.T + t) * DOWN_PITCH + c];
-    const int64_t o = (int64_t)t * p.D + n0 + c;
-    if (p.residual) v += __uint_as_float((uint32_t)p.residual[o] << 16);
-    p.out[o] = (uint16_t)pack_bf16x2(v, 0.0f);
+  for (int k = 0; k < U - 1; ++k) issue(k);
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  int sl = 0;
+  for (int v = lo; v < hi; ++v) {
+    Stream::wait();
+    issue(sl == 0 ? U - 1 : sl - 1);
+    s.consume(ring, sl, cu, acc);
+    if (++cu == units || v + 1 == hi) {
+      // the record's part of this list is done: its tokens' sums
+      const uint8_t *st = ring + sl * Stream::STAGE;
+      const int t = *(const int32_t *)(st + Stream::P_OFF + 256 * s.w + 8 * s.i16);
+      const float share = *(const float *)(st + Stream::P_OFF + 256 * s.w + 8 * s.i16 + 4);
+      if constexpr (WF == WF_INT8) acc *= *(const v4f *)(st + Stream::S_OFF + 256 * s.w + 16 * s.q);
+      if (s.i16 < recs[ca].n) {
+        v4f *sum = (v4f *)&sums[SHARED ? 0 : s.w][t][(SHARED ? 16 * s.w : 0) + 4 * s.q];
+        *sum += acc * share;
+      }
+      acc = (v4f){0.f, 0.f, 0.f, 0.f};
+      cu = 0;
+      ++ca;
+    }
+    sl = sl == U - 1 ? 0 : sl + 1;
+  }
+  wait_vmem_le<0>();                           // no DMA into the LDS of an ended workgroup
+  __syncthreads();
+  if (p.splits == 1) {
+    for (int i = threadIdx.x; i < p.T * COLS; i += 64 * EXP_WAVES) {
+      const int t = i / COLS, c = i - t * COLS;
+      if (tile0 + c >= p.D) continue;
+      const int64_t o = (int64_t)t * p.D + tile0 + c;
+      float v = sums[0][t][c];
+#pragma unroll
+      for (int k = 1; k < SETS; ++k) v += sums[k][t][c];
+      if (p.residual) v += __uint_as_float((uint32_t)p.residual[o] << 16);
+      p.out[o] = (uint16_t)pack_bf16x2(v, 0.0f);
+    }
+    return;
+  }
+  // Splits of the list: the workgroup that is done last adds their sums, in the
+  // splits' order.  The sums go through device-scope accesses, which do not
+  // stay in an XCD's own L2: each wave waits for its stores, the workgroup for
+  // its waves, and then it counts itself.  (A release fence in place of the
+  // wait writes back the whole L2, once per workgroup: 100 instead of XX us for
+  // 37 tokens, 24 experts of 2080 x 1440.)
+  const int64_t size = p.T * p.D;
+  auto at8 = [&](int k, int t, int c) { return (uint64_t *)(p.part + k * size + (int64_t)t * p.D + tile0 + c); };
+  for (int i = threadIdx.x; i < p.T * COLS / 2; i += 64 * EXP_WAVES) {
+    const int t = i / (COLS / 2), c = 2 * (i - t * (COLS / 2));
+    if (tile0 + c < p.D)
+      __hip_atomic_store(at8(split, t, c), *(const uint64_t *)&sums[0][t][c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  wait_vmem_le<0>();
+  __syncthreads();
+  if (threadIdx.x == 0) done = __hip_atomic_fetch_add(p.arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (done != p.splits - 1) return;
+  // four columns and up to four tokens per thread, the loads of several splits
+  // in flight together
+  constexpr int QUADS = COLS / 4, GROUP = 64 * EXP_WAVES / QUADS, MT = (TM + GROUP - 1) / GROUP;
+  const int c = 4 * (threadIdx.x % QUADS), t0 = threadIdx.x / QUADS;
+  if (tile0 + c >= p.D) return;                // D is a multiple of 8
+  v4f v[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) v[j] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < p.splits; ++k)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int t = t0 + j * GROUP;
+      if (t < p.T) {
+        const uint64_t u[2] = {__hip_atomic_load(at8(k, t, c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                               __hip_atomic_load(at8(k, t, c + 2), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+        v[j] += __builtin_bit_cast(v4f, u);
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int t = t0 + j * GROUP;
+    if (t >= p.T) break;
+    const int64_t o = (int64_t)t * p.D + tile0 + c;
+    if (p.residual) v[j] += load_bf16x4(p.residual + o, 4, true);
+    store_bf16x4(p.out + o, v[j], 4, true);
   }
 }
 

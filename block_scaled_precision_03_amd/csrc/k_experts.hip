@@ -17,46 +17,45 @@ struct ExpertsFormat {
   int wf;
   int64_t unit;
   bool scales;
+  int private_t;
 };
 bool experts_format(int fmt, ExpertsFormat &f) {
   switch (fmt) {
-    case MXG_INT8: f = {WF_INT8, 16, true}; return true;
-    case MXG_BF16: f = {WF_BF16, 8, false}; return true;
-    case MXG_MXFP8_E4M3: f = {WF_E4M3, 32, true}; return true;
-    case MXG_MXFP8_E5M2: f = {WF_E5M2, 32, true}; return true;
-    case MXG_MXFP4_E2M1: f = {WF_E2M1, 32, true}; return true;
-    case MXG_FP8_E4M3_BLOCK: f = {WF_BLOCK, 128, true}; return true;
+    case MXG_INT8: f = {WF_INT8, 16, true, WeightFormat<WF_INT8>::PRIVATE_T}; return true;
+    case MXG_BF16: f = {WF_BF16, 8, false, WeightFormat<WF_BF16>::PRIVATE_T}; return true;
+    case MXG_MXFP8_E4M3: f = {WF_E4M3, 32, true, WeightFormat<WF_E4M3>::PRIVATE_T}; return true;
+    case MXG_MXFP8_E5M2: f = {WF_E5M2, 32, true, WeightFormat<WF_E5M2>::PRIVATE_T}; return true;
+    case MXG_MXFP4_E2M1: f = {WF_E2M1, 32, true, WeightFormat<WF_E2M1>::PRIVATE_T}; return true;
+    case MXG_FP8_E4M3_BLOCK: f = {WF_BLOCK, 128, true, WeightFormat<WF_BLOCK>::PRIVATE_T}; return true;
     default: return false;
   }
 }
 
-// Workspace: h's two planes, the count of live experts, their records, the pairs.
+// Workspace: h's two planes, the counts, the records, the pairs, the splits' sums.
 struct ExpertsSpace {
-  int64_t live, rec, pair, bytes;
+  int64_t count, rec, pair, part, bytes;
 };
 ExpertsSpace experts_space(int64_t T, int topk, int64_t F) {
+  const int64_t P = T * topk;
   ExpertsSpace s;
-  s.live = up16(4 * T * topk * F);
-  s.rec = s.live + 16;
-  s.pair = s.rec + T * topk * (int64_t)sizeof(ExpertRec);
-  s.bytes = s.pair + T * topk * (int64_t)sizeof(ExpertPair);
+  s.count = up16(4 * P * F);
+  s.rec = s.count + 16 + 4 * EXP_SPLIT_BLOCKS;
+  s.pair = s.rec + P * (int64_t)sizeof(ExpertRec);
+  s.part = up16(s.pair + P * (int64_t)sizeof(ExpertPair));
+  s.bytes = s.part + 4 * T * 64 * EXP_SPLIT_BLOCKS;
   return s;
 }
 
-template <int FMAX>
-void launch_experts(int wf, const ExpertsArgs &a, unsigned up, unsigned down, hipStream_t stream) {
-  auto go = [&](auto fc) {
-    constexpr int WF = decltype(fc)::value;
-    hipLaunchKernelGGL((experts_up_kernel<WF, FMAX>), dim3(up), dim3(64 * UP_WAVES), 0, stream, a);
-    hipLaunchKernelGGL((experts_down_kernel<WF, FMAX>), dim3(down), dim3(64 * DOWN_WAVES), down_lds_bytes(a.T), stream, a);
-  };
-  switch (wf) {
-    case WF_INT8: go(std::integral_constant<int, WF_INT8>{}); break;
-    case WF_BF16: go(std::integral_constant<int, WF_BF16>{}); break;
-    case WF_E4M3: go(std::integral_constant<int, WF_E4M3>{}); break;
-    case WF_E5M2: go(std::integral_constant<int, WF_E5M2>{}); break;
-    case WF_E2M1: go(std::integral_constant<int, WF_E2M1>{}); break;
-    default: go(std::integral_constant<int, WF_BLOCK>{}); break;
+template <int WF>
+void launch_experts(const ExpertsArgs &a, unsigned up, unsigned down, hipStream_t stream) {
+  const dim3 threads(64 * EXP_WAVES);
+  if (a.T <= WeightFormat<WF>::PRIVATE_T) {
+    hipLaunchKernelGGL((experts_up_kernel<WF, false>), dim3(up), threads, 0, stream, a);
+    hipLaunchKernelGGL((experts_down_kernel<WF, false, WeightFormat<WF>::PRIVATE_T>), dim3(down), threads, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((experts_up_kernel<WF, true>), dim3(up), threads, 0, stream, a);
+    if (a.T <= 16) hipLaunchKernelGGL((experts_down_kernel<WF, true, 16>), dim3(down), threads, 0, stream, a);
+    else hipLaunchKernelGGL((experts_down_kernel<WF, true, EXP_MAX_T>), dim3(down), threads, 0, stream, a);
   }
 }
 
@@ -64,7 +63,7 @@ void launch_experts(int wf, const ExpertsArgs &a, unsigned up, unsigned down, hi
 
 int experts_init() {
   hipFuncAttributes attr;
-  return hipFuncGetAttributes(&attr, (const void *)experts_up_kernel<WF_INT8, 1>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
+  return hipFuncGetAttributes(&attr, (const void *)experts_up_kernel<WF_INT8, false>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
 }
 
 }  // namespace mxg
@@ -90,8 +89,8 @@ extern "C" int moe_experts_validate(int fmt, const void *x, const int32_t *ids, 
   if (!out || !ids || !weights || !workspace) return MXG_ERR_INVALID_ARG;
   if (workspace_bytes < experts_space(T, topk, F).bytes) return MXG_ERR_INVALID_ARG;
   if (F > 0 && (!x || !w1 || !w2 || (f.scales && (!s1 || !s2)))) return MXG_ERR_INVALID_ARG;
-  // INT8 and block scales are FP32; E8M0 scales are bytes
-  const uintptr_t sa = f.wf == WF_INT8 || f.wf == WF_BLOCK ? 4 : 1;
+  // INT8 and block scales are FP32; E8M0 scales are read in aligned words
+  const uintptr_t sa = f.wf == WF_INT8 || f.wf == WF_BLOCK ? 4 : 16;
   if (!aligned(out, 16) || !aligned(residual, 16) || !aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) ||
       !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(s1, sa) || !aligned(s2, sa))
     return MXG_ERR_MISALIGNED;
@@ -120,9 +119,11 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   a.residual = (const uint16_t *)residual;
   a.out = (uint16_t *)out;
   a.h = (uint16_t *)ws;
-  a.live = (int32_t *)(ws + sp.live);
+  a.count = (int32_t *)(ws + sp.count);
+  a.arrived = a.count + 4;
   a.rec = (ExpertRec *)(ws + sp.rec);
   a.pair = (ExpertPair *)(ws + sp.pair);
+  a.part = (float *)(ws + sp.part);
   a.D = D;
   a.F = F;
   a.N1 = activation == MXG_ACT_SWIGLU ? 2 * F : F;
@@ -130,13 +131,24 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   a.E = (int)E;
   a.topk = topk;
   a.act = activation;
-  a.tiles = (int)cdiv(a.N1, 16 * UP_FN);
-  const int64_t most = std::min<int64_t>(E, T * topk);   // live experts at most
-  // Parts of K per expert, so that few experts give every wave work.  F = 0:
-  // none, and neither weights nor scales (which may be null) are touched.
-  a.parts = F == 0 ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>(DOWN_WAVES, cdiv(2 * DOWN_WAVES, most)));
-  const unsigned up = (unsigned)(1 + most * a.tiles), down = (unsigned)cdiv(D, 16 * DOWN_FN);
-  if (T <= 16) launch_experts<1>(f.wf, a, up, down, stream);
-  else launch_experts<4>(f.wf, a, up, down, stream);
+  const bool few = T <= f.private_t;
+  const int rows = few ? 16 : 16 * EXP_WAVES;
+  a.up_tiles = (int)cdiv(a.N1, rows);
+  a.down_tiles = (int)cdiv(D, rows);
+  // Few columns leave compute units idle: the records are split over several
+  // workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds their sums).
+  a.splits = few ? 1 : (int)std::max<int64_t>(1, EXP_SPLIT_BLOCKS / a.down_tiles);
+  // records: experts with tokens, and one more per 16 tokens of an expert
+  const int64_t P = T * topk, live = std::min<int64_t>(E, P), most = live + (P - live) / EXP_ROWS;
+  // F = 0: no tiles, no list; neither weights nor scales (which may be null) are touched
+  const unsigned up = (unsigned)(1 + most * a.up_tiles), down = (unsigned)(a.down_tiles * a.splits);
+  switch (f.wf) {
+    case WF_INT8: launch_experts<WF_INT8>(a, up, down, stream); break;
+    case WF_BF16: launch_experts<WF_BF16>(a, up, down, stream); break;
+    case WF_E4M3: launch_experts<WF_E4M3>(a, up, down, stream); break;
+    case WF_E5M2: launch_experts<WF_E5M2>(a, up, down, stream); break;
+    case WF_E2M1: launch_experts<WF_E2M1>(a, up, down, stream); break;
+    default: launch_experts<WF_BLOCK>(a, up, down, stream); break;
+  }
   return launch_status();
 }

@@ -706,8 +706,8 @@ enum { MXG_FP8_E4M3_BLOCK = 18 };
  * T <= 64 (more: the grouped products), E <= 1024, topk <= 32, D and F <= 131072,
  * both multiples of 16 (INT8), 8 (BF16), 32 (MX) or 128 (block): else
  * MXG_ERR_UNSUPPORTED; an unknown enum, null pointer, negative size, E or topk
- * below 1 or a small workspace is MXG_ERR_INVALID_ARG; x, weights, residual, out
- * and workspace 16-byte aligned, FP32 and int32 arrays 4-byte.  T or D = 0:
+ * below 1 or a small workspace is MXG_ERR_INVALID_ARG; x, w1, w2, E8M0 scales,
+ * residual, out and workspace 16-byte aligned, FP32 and int32 arrays 4-byte.  T or D = 0:
  * no-op; F = 0: out = residual (or 0).  The sums' order is fixed: the same call
  * gives the same bits.  Device ids are never read by the host.
  */

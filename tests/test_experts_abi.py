@@ -23,7 +23,7 @@ def ok(**kw):
 
 GOOD = [dict(), dict(residual=None), dict(T=64), dict(E=1024), dict(topk=32), dict(E=1, topk=2), dict(activation=0),
         dict(activation=3), dict(ids=P + 4), dict(weights=P + 4), dict(s1=P + 4), dict(T=0, x=0, ids=0, out=0, workspace=None),
-        dict(D=0, out=0), dict(F=0, w1=0, w2=0, x=0), dict(fmt=R.BF16, s1=0, s2=0, D=8, F=8), dict(fmt=R.E4M3, s1=P + 1, s2=P + 3),
+        dict(D=0, out=0), dict(F=0, w1=0, w2=0, x=0), dict(fmt=R.BF16, s1=0, s2=0, D=8, F=8), dict(fmt=R.E4M3, s1=P + 16),
         dict(fmt=R.E5M2), dict(fmt=R.E2M1, D=32, F=96), dict(fmt=R.BLOCK, D=128, F=256), dict(D=131072, F=131072)]
 BAD = [(dict(fmt=16), -1), (dict(fmt=65), -1), (dict(fmt=2), -1), (dict(fmt=R.E4M3 | 0x100), -1),
        (dict(activation=4), -1), (dict(activation=-1), -1), (dict(activation=9), -1),
@@ -34,7 +34,8 @@ BAD = [(dict(fmt=16), -1), (dict(fmt=65), -1), (dict(fmt=2), -1), (dict(fmt=R.E4
        (dict(x=0), -1), (dict(ids=0), -1), (dict(weights=0), -1), (dict(w1=0), -1), (dict(s1=0), -1), (dict(w2=0), -1),
        (dict(s2=0), -1), (dict(out=0), -1), (dict(workspace=None), -1), (dict(fmt=R.E4M3, s2=0), -1),
        (dict(x=P + 8), -3), (dict(out=P + 2), -3), (dict(residual=P + 2), -3), (dict(w1=P + 8), -3), (dict(w2=P + 4), -3),
-       (dict(ids=P + 2), -3), (dict(weights=P + 1), -3), (dict(s1=P + 2), -3), (dict(workspace=P + 8), -3)]
+       (dict(ids=P + 2), -3), (dict(weights=P + 1), -3), (dict(s1=P + 2), -3), (dict(fmt=R.E4M3, s2=P + 8), -3),
+       (dict(workspace=P + 8), -3)]
 
 
 @pytest.mark.parametrize("kw", GOOD)
