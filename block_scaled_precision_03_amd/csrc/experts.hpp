@@ -29,7 +29,7 @@ namespace mxg {
 
 enum : int { WF_INT8 = 0, WF_BF16 = 1, WF_E4M3 = 2, WF_E5M2 = 3, WF_E2M1 = 4, WF_BLOCK = 5 };
 constexpr int EXP_MAX_T = 64, EXP_MAX_E = 1024, EXP_MAX_TOPK = 32;
-constexpr int EXP_ROWS = 16;                   // tokens of a record
+constexpr int EXP_ROWS = 16;                   // tokens of a record at most
 constexpr int EXP_WAVES = 4;
 constexpr int EXP_SPLIT_BLOCKS = 512;          // workgroups of the second kernel that splits of the list may make
 
@@ -58,6 +58,7 @@ struct ExpertsArgs {
   int64_t D, F, N1;                            // N1 rows of W1[e]: F or 2 F
   int T, E, topk, act;
   int up_tiles, down_tiles, splits;
+  int rows;                                    // tokens of a record at most: 8 or 16
 };
 
 // What 16 bytes of a row hold.
@@ -113,9 +114,9 @@ __device__ inline bf16x8_t weight_values(const v4i &raw, int m, float scale) {
 // which stages have landed: stages that do not exist are asked for past the end
 // of their resources, which writes zeros and reads no memory.
 //
-// LDS of a stage: [W: 4 x 2 KiB][X: PL planes][S: 4 x 256 B][pairs: 4 x 128 B],
-// a quarter of W, S and the pairs per wave; X a quarter per wave (private) or
-// whole (shared).
+// LDS of a stage: [W: 4 x 2 KiB][X][S: 4 x 256 B][pairs],
+// a quarter of W and S per wave; X and the pairs a quarter per wave (private)
+// or for all (shared).
 //   W: row r of 128 bytes, 16-byte piece p at position p ^ kswz(r); lane (i, q)
 //     of a matrix instruction takes pieces q and q + 4 of row i.
 //   X: rows of XPITCH bytes, piece p at position p ^ xswz(r): the values beside
@@ -125,22 +126,23 @@ __device__ inline bf16x8_t weight_values(const v4i &raw, int m, float scale) {
 //     when it is shifted by the XOR of their pieces (1, 2 or 4).
 //   S: the aligned dwords around a row's E8M0 scales of the unit (2 per row,
 //     E2M1 4); the channel scales (INT8, DOWN); the unit's block scale.
-template <int WF, int PL, bool SHARED, bool DOWN, int U>
+template <int WF, int PL, int ROWS, bool DOWN, int U>
 struct ExpertStream {
+  static constexpr bool SHARED = ROWS > 0;     // activation rows of a shared stage; 0: private
   typedef WeightFormat<WF> F;
-  static constexpr int RC = SHARED ? EXP_ROWS : F::PRIVATE_T;
-  // shared: XI DMAs per wave and plane, a plane after the other; private: one
-  // DMA, RC rows of each plane
-  static constexpr int XI = SHARED ? (RC * F::XPITCH / EXP_WAVES + 1023) / 1024 : 1;
-  static constexpr int XD = SHARED ? PL * XI : 1;                                       // DMAs per wave
-  static constexpr int XPLANE = SHARED ? EXP_WAVES * XI * 1024 : RC * F::XPITCH;
-  static constexpr int XSIZE = SHARED ? PL * XPLANE : EXP_WAVES * 1024;
-  static_assert(SHARED || PL * RC * F::XPITCH <= 1024, "one DMA");
+  static constexpr int RC = SHARED ? ROWS : F::PRIVATE_T;
+  // the rows of one plane after the other, in DMAs of 1 KiB: shared, a share
+  // of them per wave (the same number for each); private, one
+  static constexpr int XPLANE = RC * F::XPITCH;
+  static constexpr int XD = SHARED ? (PL * XPLANE + EXP_WAVES * 1024 - 1) / (EXP_WAVES * 1024) : 1;   // DMAs per wave
+  static constexpr int XSIZE = EXP_WAVES * XD * 1024;
+  static_assert(SHARED || PL * XPLANE <= 1024, "one DMA");
   static constexpr bool S = F::MX || WF == WF_BLOCK || (DOWN && WF == WF_INT8);
   static constexpr int W_OFF = 0, X_OFF = EXP_WAVES * 2048;
   static constexpr int S_OFF = X_OFF + XSIZE;
   static constexpr int P_OFF = S_OFF + (S ? EXP_WAVES * 256 : 0);
-  static constexpr int STAGE = P_OFF + (DOWN ? EXP_WAVES * 256 : 0);
+  // every wave brings the record's pairs, shared to the same place
+  static constexpr int STAGE = P_OFF + (DOWN ? (SHARED ? 256 : EXP_WAVES * 256) : 0);
   static constexpr int LDS_BYTES = U * STAGE;
   static constexpr int DMAS = 2 + XD + (S ? 1 : 0) + (DOWN ? 1 : 0);
   static_assert((U - 1) * DMAS < 64, "vmcnt is 6 bits");
@@ -155,7 +157,7 @@ struct ExpertStream {
   uint32_t lds0;
   uint32_t KB, K, SK, units;
   uint32_t vo, vo_tail;                        // weight rows: lane offsets; in the last unit
-  uint32_t xv[XI], xv_tail[XI];                // activation rows
+  uint32_t xv[XD], xv_tail[XD];                // activation rows
   uint32_t xplane;                             // bytes between planes in memory
   u32x4 rw, rs, rx, rp;
   uint32_t pair0;                              // byte offset of the record's pairs
@@ -178,7 +180,7 @@ struct ExpertStream {
     rw = rs = rp = rsrc4(smem, 0);             // until the first record: nothing
     pair0 = 0;
 #pragma unroll
-    for (int k = 0; k < XI; ++k) xv[k] = xv_tail[k] = NOWHERE;
+    for (int k = 0; k < XD; ++k) xv[k] = xv_tail[k] = NOWHERE;
   }
   static constexpr uint32_t NOWHERE = 0x80000000u;
 
@@ -195,10 +197,9 @@ struct ExpertStream {
   template <class RowAt>
   __device__ inline void set_rows(int n, RowAt row_at) {
 #pragma unroll
-    for (int k = 0; k < XI; ++k) {
-      const int at = ((SHARED ? w * XI : 0) + k) * 1024 + 16 * lane;
-      const int row = at / F::XPITCH, pl = SHARED ? 0 : row / RC, r = SHARED ? row : row % RC;
-      const int piece = (at % F::XPITCH / 16) ^ xswz(r);
+    for (int k = 0; k < XD; ++k) {
+      const int at = ((SHARED ? w * XD : 0) + k) * 1024 + 16 * lane, row = at / F::XPITCH;
+      const int pl = row / RC, r = row % RC, piece = (at % F::XPITCH / 16) ^ xswz(r);
       xv[k] = r < n && pl < PL ? row_at(r) + pl * xplane + 16u * piece : NOWHERE;
       xv_tail[k] = (units - 1) * F::UNIT + 8u * piece < K ? xv[k] : NOWHERE;
     }
@@ -212,13 +213,10 @@ struct ExpertStream {
     const uint32_t wd = st + W_OFF + 2048u * w;
     dma_asm_v<16, 0>(wd, rw, vw, live ? 128u * u : 0u);
     dma_asm_v<16, 1024>(wd, rw, vw, live ? 128u * u + 8u * KB : 0u);
-    const uint32_t xd = st + X_OFF + (SHARED ? (uint32_t)w * XI * 1024u : (uint32_t)w * 1024u);
-    static_for<0, SHARED ? PL : 1>([&](auto pc) {
-      static_for<0, XI>([&](auto kc) {
-        constexpr int p = decltype(pc)::value, k = decltype(kc)::value;
-        const uint32_t v = !live ? NOWHERE : last ? xv_tail[k] : xv[k];
-        dma_asm_v<16, p * XPLANE + k * 1024>(xd, rx, v, live ? u * F::XPITCH + p * xplane : 0u);
-      });
+    const uint32_t xd = st + X_OFF + 1024u * XD * (uint32_t)w;
+    static_for<0, XD>([&](auto kc) {
+      constexpr int k = decltype(kc)::value;
+      dma_asm_v<16, k * 1024>(xd, rx, !live ? NOWHERE : last ? xv_tail[k] : xv[k], live ? u * F::XPITCH : 0u);
     });
     if constexpr (S) {
       uint32_t v = NOWHERE;
@@ -229,7 +227,7 @@ struct ExpertStream {
       dma_asm_v<4>(st + S_OFF + 256u * w, rs, live ? v : NOWHERE, 0u);
     }
     if constexpr (DOWN)
-      dma_asm_v<4>(st + P_OFF + 256u * w, rp, live && lane < 32 ? 4u * lane : NOWHERE, live ? pair0 : 0u);
+      dma_asm_v<4>(st + P_OFF + (SHARED ? 0u : 256u * w), rp, live && lane < 32 ? 4u * lane : NOWHERE, live ? pair0 : 0u);
   }
 
   // Stage v has landed once at most the later stages' DMAs are outstanding
@@ -298,12 +296,12 @@ __device__ inline uint64_t expert_mask(const ExpertMasks &mk, int e) {
 }
 
 // For 64 experts, one per lane: their tokens n, and before each of them the
-// records (16 tokens or fewer each) and the pairs, of these 64.
+// records (p.rows tokens or fewer each) and the pairs, of these 64.
 __device__ inline void expert_scan(const ExpertsArgs &p, const ExpertMasks &mk, int e, int &n, int &recs, int &pairs,
                                    int &all_recs, int &all_pairs) {
   const int lane = threadIdx.x & 63;
   n = e < p.E ? __popcll(expert_mask(mk, e)) : 0;
-  const int mine = (n + EXP_ROWS - 1) / EXP_ROWS << 16 | n;     // both counts stay below 2^12
+  const int mine = (n + p.rows - 1) / p.rows << 16 | n;     // both counts stay below 2^12
   int sum = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -325,13 +323,13 @@ __device__ inline ExpertRec find_record(const ExpertsArgs &p, const ExpertMasks 
     int n, recs, pairs, all_recs, all_pairs;
     expert_scan(p, mk, e0 + lane, n, recs, pairs, all_recs, all_pairs);
     if (rank < all_recs) {
-      const uint64_t me = __ballot(n > 0 && recs <= rank && rank < recs + (n + EXP_ROWS - 1) / EXP_ROWS);
+      const uint64_t me = __ballot(n > 0 && recs <= rank && rank < recs + (n + p.rows - 1) / p.rows);
       const int l = __ffsll((unsigned long long)me) - 1;
-      const int skip = EXP_ROWS * (rank - __shfl(recs, l));
+      const int skip = p.rows * (rank - __shfl(recs, l));
       tokens = expert_mask(mk, e0 + l);
       for (int k = 0; k < skip; ++k) tokens &= tokens - 1;
       const int left = __shfl(n, l) - skip;
-      return ExpertRec{e0 + l, base + __shfl(pairs, l) + skip, left < EXP_ROWS ? left : EXP_ROWS, 0};
+      return ExpertRec{e0 + l, base + __shfl(pairs, l) + skip, left < p.rows ? left : p.rows, 0};
     }
     rank -= all_recs;
     base += all_pairs;
@@ -351,9 +349,8 @@ __device__ inline void expert_table(const ExpertsArgs &p, const ExpertMasks &mk,
       int n, recs, pairs, all_recs, all_pairs;
       expert_scan(p, mk, e0 + lane, n, recs, pairs, all_recs, all_pairs);
       if (e0 + lane < p.E) first[e0 + lane] = pair0 + pairs;
-      for (int k = 0; k < n; k += EXP_ROWS)
-        p.rec[rec0 + recs + k / EXP_ROWS] =
-            ExpertRec{e0 + lane, pair0 + pairs + k, n - k < EXP_ROWS ? n - k : EXP_ROWS, 0};
+      for (int k = 0; k < n; k += p.rows)
+        p.rec[rec0 + recs + k / p.rows] = ExpertRec{e0 + lane, pair0 + pairs + k, n - k < p.rows ? n - k : p.rows, 0};
       rec0 += all_recs;
       pair0 += all_pairs;
     }
@@ -405,10 +402,12 @@ __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v
   }
 }
 
-template <int WF, bool SHARED>
+// ROWS: the most tokens of a record, shared; 0: private.
+template <int WF, int ROWS>
 __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs p) {
-  constexpr int U = SHARED ? 4 : 6, ROWS = SHARED ? 16 * EXP_WAVES : 16;
-  typedef ExpertStream<WF, 1, SHARED, false, U> Stream;
+  constexpr bool SHARED = ROWS > 0;
+  constexpr int U = SHARED ? 4 : 6, TILE = SHARED ? 16 * EXP_WAVES : 16;
+  typedef ExpertStream<WF, 1, ROWS, false, U> Stream;
   __shared__ __attribute__((aligned(1024))) union {
     struct {
       ExpertMasks mk;
@@ -431,12 +430,12 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
   if (rec.n == 0) return;
   const int lane = threadIdx.x & 63;
   const int place = __popcll(tokens & ((1ull << lane) - 1));
-  if (threadIdx.x < 64 && (tokens >> lane & 1) && place < EXP_ROWS) tok[place] = lane;
+  if (threadIdx.x < 64 && (tokens >> lane & 1) && place < p.rows) tok[place] = lane;
   __syncthreads();                             // and the masks' memory is free from here on
 
   Stream s;
   s.init(sm.ring, p.D, rsrc4(p.x, clamp_records(2 * p.T * p.D)), 0u);
-  const int64_t n0 = (int64_t)tile * ROWS + (SHARED ? 16 * s.w : 0);
+  const int64_t n0 = (int64_t)tile * TILE + (SHARED ? 16 * s.w : 0);
   s.set_weight(p.w1, p.s1, rec.e, p.N1, n0);
   s.set_rows(rec.n, [&](int r) { return (uint32_t)(2 * tok[r] * p.D); });
   const int c = 4 * s.q;
@@ -473,11 +472,12 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
 }
 
 // TM: the most tokens (the sums' rows).
-template <int WF, bool SHARED, int TM>
+template <int WF, int ROWS, int TM>
 __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int U = !SHARED ? 5 : TM > 16 ? 3 : 4, COLS = SHARED ? 16 * EXP_WAVES : 16, SETS = SHARED ? 1 : EXP_WAVES;
+  constexpr bool SHARED = ROWS > 0;
+  constexpr int U = !SHARED ? 5 : TM > 16 && ROWS > 8 ? 3 : 4, COLS = SHARED ? 16 * EXP_WAVES : 16, SETS = SHARED ? 1 : EXP_WAVES;
   constexpr int PITCH = COLS + 4;              // floats per token: columns and a skew
-  typedef ExpertStream<WF, 2, SHARED, true, U> Stream;
+  typedef ExpertStream<WF, 2, ROWS, true, U> Stream;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[Stream::LDS_BYTES];
   __shared__ __attribute__((aligned(16))) float sums[SETS][TM][PITCH];
   __shared__ int32_t done;
@@ -527,8 +527,8 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
     if (++cu == units || v + 1 == hi) {
       // the record's part of this list is done: its tokens' sums
       const uint8_t *st = ring + sl * Stream::STAGE;
-      const int t = *(const int32_t *)(st + Stream::P_OFF + 256 * s.w + 8 * s.i16);
-      const float share = *(const float *)(st + Stream::P_OFF + 256 * s.w + 8 * s.i16 + 4);
+      const int t = *(const int32_t *)(st + Stream::P_OFF + (SHARED ? 0 : 256 * s.w) + 8 * s.i16);
+      const float share = *(const float *)(st + Stream::P_OFF + (SHARED ? 0 : 256 * s.w) + 8 * s.i16 + 4);
       if constexpr (WF == WF_INT8) acc *= *(const v4f *)(st + Stream::S_OFF + 256 * s.w + 16 * s.q);
       if (s.i16 < recs[ca].n) {
         v4f *sum = (v4f *)&sums[SHARED ? 0 : s.w][t][(SHARED ? 16 * s.w : 0) + 4 * s.q];
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
   // splits' order.  The sums go through device-scope accesses, which do not
   // stay in an XCD's own L2: each wave waits for its stores, the workgroup for
   // its waves, and then it counts itself.  (A release fence in place of the
-  // wait writes back the whole L2, once per workgroup: 100 instead of XX us for
+  // wait writes back the whole L2, once per workgroup: 100 instead of 40 us for
   // 37 tokens, 24 experts of 2080 x 1440.)
   const int64_t size = p.T * p.D;
   auto at8 = [&](int k, int t, int c) { return (uint64_t *)(p.part + k * size + (int64_t)t * p.D + tile0 + c); };
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
   v4f v[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) v[j] = (v4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < p.splits; ++k)
 #pragma unroll
     for (int j = 0; j < MT; ++j) {

@@ -46,24 +46,27 @@ ExpertsSpace experts_space(int64_t T, int topk, int64_t F) {
   return s;
 }
 
+template <int WF, int ROWS, int TM>
+void launch_pair(const ExpertsArgs &a, unsigned up, unsigned down, hipStream_t stream) {
+  hipLaunchKernelGGL((experts_up_kernel<WF, ROWS>), dim3(up), dim3(64 * EXP_WAVES), 0, stream, a);
+  hipLaunchKernelGGL((experts_down_kernel<WF, ROWS, TM>), dim3(down), dim3(64 * EXP_WAVES), 0, stream, a);
+}
+
 template <int WF>
 void launch_experts(const ExpertsArgs &a, unsigned up, unsigned down, hipStream_t stream) {
-  const dim3 threads(64 * EXP_WAVES);
-  if (a.T <= WeightFormat<WF>::PRIVATE_T) {
-    hipLaunchKernelGGL((experts_up_kernel<WF, false>), dim3(up), threads, 0, stream, a);
-    hipLaunchKernelGGL((experts_down_kernel<WF, false, WeightFormat<WF>::PRIVATE_T>), dim3(down), threads, 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((experts_up_kernel<WF, true>), dim3(up), threads, 0, stream, a);
-    if (a.T <= 16) hipLaunchKernelGGL((experts_down_kernel<WF, true, 16>), dim3(down), threads, 0, stream, a);
-    else hipLaunchKernelGGL((experts_down_kernel<WF, true, EXP_MAX_T>), dim3(down), threads, 0, stream, a);
-  }
+  constexpr int FEW = WeightFormat<WF>::PRIVATE_T;
+  if (a.T <= FEW) launch_pair<WF, 0, FEW>(a, up, down, stream);
+  else if (a.T <= 16 && a.rows == 8) launch_pair<WF, 8, 16>(a, up, down, stream);
+  else if (a.T <= 16) launch_pair<WF, 16, 16>(a, up, down, stream);
+  else if (a.rows == 8) launch_pair<WF, 8, EXP_MAX_T>(a, up, down, stream);
+  else launch_pair<WF, 16, EXP_MAX_T>(a, up, down, stream);
 }
 
 }  // namespace
 
 int experts_init() {
   hipFuncAttributes attr;
-  return hipFuncGetAttributes(&attr, (const void *)experts_up_kernel<WF_INT8, false>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
+  return hipFuncGetAttributes(&attr, (const void *)experts_up_kernel<WF_INT8, 0>) == hipSuccess ? MXG_OK : MXG_ERR_HIP;
 }
 
 }  // namespace mxg
@@ -139,7 +142,12 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   // workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds their sums).
   a.splits = few ? 1 : (int)std::max<int64_t>(1, EXP_SPLIT_BLOCKS / a.down_tiles);
   // records: experts with tokens, and one more per 16 tokens of an expert
-  const int64_t P = T * topk, live = std::min<int64_t>(E, P), most = live + (P - live) / EXP_ROWS;
+  const int64_t P = T * topk, live = std::min<int64_t>(E, P);
+  // Up to 5 tokens per expert that has any: records of 8, whose smaller
+  // stages leave room for more of them in flight; else 16 (an expert of more
+  // tokens than that is read again).
+  a.rows = P <= 5 * live ? 8 : EXP_ROWS;
+  const int64_t most = live + (P - live) / a.rows;
   // F = 0: no tiles, no list; neither weights nor scales (which may be null) are touched
   const unsigned up = (unsigned)(1 + most * a.up_tiles), down = (unsigned)(a.down_tiles * a.splits);
   switch (f.wf) {
