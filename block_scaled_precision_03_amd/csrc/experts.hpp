@@ -18,8 +18,10 @@
 // No sum's order depends on timing.
 //
 // Two ways of sharing the work of a workgroup's four waves:
-//   private (one or two tokens): 16 rows of the weight, K (down: the list) split
-//     over the waves, each with its own ring of stages; they meet at the end.
+//   private (one or two tokens): each wave has a ring of stages of its own; up:
+//     64 rows of the weight, 16 per wave, or, where that makes too few
+//     workgroups, 16 rows with K split over the waves; down: 16 rows (columns
+//     of out), the list split over the waves, whose sums meet at the end.
 //   shared: 64 rows, 16 per wave, one ring; the activations of a stage, up to 16
 //     rows of them, are brought once for all four waves.
 #pragma once
@@ -59,6 +61,7 @@ struct ExpertsArgs {
   int T, E, topk, act;
   int up_tiles, down_tiles, splits;
   int rows;                                    // tokens of a record at most: 8 or 16
+  bool split_k;                                // private, up: K split over the waves, else 16 rows each
 };
 
 // What 16 bytes of a row hold.
@@ -371,6 +374,74 @@ __device__ inline void expert_table(const ExpertsArgs &p, const ExpertMasks &mk,
   }
 }
 
+// The same for at most 64 slots (one or two tokens), in the registers of every
+// wave, without LDS or barriers: lane s holds slot s.  Records come in the
+// order of the slots that first name their experts.
+struct SlotTable {
+  int e, t;                                    // expert (-1: none) and token of the lane's slot
+  int head;                                    // first lane with this expert
+  uint32_t tokens;                             // tokens that name it
+  int base;                                    // its first pair
+  float share;                                 // of the lane's token
+  bool lead;                                   // first slot of its token with this expert
+  uint64_t heads;                              // lanes that are their expert's first
+};
+
+__device__ inline SlotTable slot_table(const ExpertsArgs &p) {
+  const int lane = threadIdx.x & 63, P = p.T * p.topk;
+  const uint64_t below = (1ull << lane) - 1;
+  SlotTable s;
+  s.e = -1;
+  s.t = lane / p.topk;
+  float w = 0.0f;
+  if (lane < P) {
+    s.e = p.ids[lane];
+    w = p.w[lane];
+    if (s.e < 0 || s.e >= p.E) s.e = -1;
+  }
+  s.head = lane;
+  s.tokens = 0;
+  s.share = 0.0f;
+  s.lead = s.e >= 0;
+  for (int k = P - 1; k >= 0; --k) {
+    const int e = __builtin_amdgcn_readlane(s.e, k), t = k >= p.topk;
+    if (s.e >= 0 && e == s.e) {
+      s.head = k < s.head ? k : s.head;
+      s.tokens |= 1u << t;
+      if (t == s.t && k < lane) s.lead = false;
+    }
+  }
+  for (int k = 0; k < P; ++k) {
+    const int e = __builtin_amdgcn_readlane(s.e, k), t = k >= p.topk;
+    const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
+    if (s.e >= 0 && e == s.e && t == s.t) s.share += wk;
+  }
+  s.heads = __ballot(s.e >= 0 && s.head == lane);
+  const uint64_t both = __ballot(s.tokens == 3u) & s.heads;
+  s.base = __popcll(s.heads & below) + __popcll(both & below);
+  return s;
+}
+
+// Record `rank` (n = 0: there is none) and its tokens as bits.
+__device__ inline ExpertRec find_record(const SlotTable &s, int rank, uint64_t &tokens) {
+  const int lane = threadIdx.x & 63;
+  tokens = 0;
+  if (rank >= __popcll(s.heads)) return ExpertRec{0, 0, 0, 0};
+  const uint64_t me = __ballot((s.heads >> lane & 1) && __popcll(s.heads & ((1ull << lane) - 1)) == rank);
+  const int l = __ffsll((unsigned long long)me) - 1;
+  tokens = (uint32_t)__shfl((int)s.tokens, l);
+  return ExpertRec{__shfl(s.e, l), __shfl(s.base, l), (int32_t)__popcll(tokens), 0};
+}
+
+__device__ inline void expert_table(const ExpertsArgs &p, const SlotTable &s) {
+  const int lane = threadIdx.x & 63;
+  const int base = __shfl(s.base, s.head);
+  if (threadIdx.x >= 64) return;
+  if (lane == 0) *p.count = __popcll(s.heads);
+  if (s.heads >> lane & 1) p.rec[__popcll(s.heads & ((1ull << lane) - 1))] = ExpertRec{s.e, s.base, (int32_t)__popc(s.tokens), 0};
+  if (s.lead) p.pair[base + (s.t == 1 && (s.tokens & 1u) ? 1 : 0)] = ExpertPair{s.t, s.share};
+}
+
 // h of four consecutive rows of W1 (two SwiGLU pairs), as two BF16 each.
 __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v4f &z) {
   const int64_t plane = (int64_t)p.T * p.topk * p.F;
@@ -406,7 +477,7 @@ __device__ inline void store_h(const ExpertsArgs &p, int row, int64_t n, const v
 template <int WF, int ROWS>
 __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs p) {
   constexpr bool SHARED = ROWS > 0;
-  constexpr int U = SHARED ? 4 : 6, TILE = SHARED ? 16 * EXP_WAVES : 16;
+  constexpr int U = 4;
   typedef ExpertStream<WF, 1, ROWS, false, U> Stream;
   __shared__ __attribute__((aligned(1024))) union {
     struct {
@@ -417,27 +488,42 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
     v4f part[EXP_WAVES][64];
   } sm;
   __shared__ int32_t tok[EXP_ROWS];
-  expert_masks(p, sm.t.mk);
-  if (blockIdx.x == 0) {
-    expert_table(p, sm.t.mk, sm.t.first);
-    return;
-  }
-  const int rank = (int)(blockIdx.x - 1) / p.up_tiles, tile = (int)(blockIdx.x - 1) - rank * p.up_tiles;
+  const int rank = (int)(blockIdx.x - 1) / max(p.up_tiles, 1), tile = (int)(blockIdx.x - 1) - rank * p.up_tiles;
   uint64_t tokens;
-  ExpertRec rec = find_record(p, sm.t.mk, rank, tokens);
+  ExpertRec rec;
+  if constexpr (SHARED) {
+    expert_masks(p, sm.t.mk);
+    if (blockIdx.x == 0) {
+      expert_table(p, sm.t.mk, sm.t.first);
+      return;
+    }
+    rec = find_record(p, sm.t.mk, rank, tokens);
+  } else {
+    const SlotTable slots = slot_table(p);
+    if (blockIdx.x == 0) {
+      expert_table(p, slots);
+      return;
+    }
+    rec = find_record(slots, rank, tokens);
+  }
   rec.e = __builtin_amdgcn_readfirstlane(rec.e);
   rec.n = __builtin_amdgcn_readfirstlane(rec.n);
   if (rec.n == 0) return;
-  const int lane = threadIdx.x & 63;
-  const int place = __popcll(tokens & ((1ull << lane) - 1));
-  if (threadIdx.x < 64 && (tokens >> lane & 1) && place < p.rows) tok[place] = lane;
-  __syncthreads();                             // and the masks' memory is free from here on
+  if constexpr (SHARED) {
+    const int lane = threadIdx.x & 63, place = __popcll(tokens & ((1ull << lane) - 1));
+    if (threadIdx.x < 64 && (tokens >> lane & 1) && place < p.rows) tok[place] = lane;
+    __syncthreads();                           // and the masks' memory is free from here on
+  }
 
   Stream s;
   s.init(sm.ring, p.D, rsrc4(p.x, clamp_records(2 * p.T * p.D)), 0u);
-  const int64_t n0 = (int64_t)tile * TILE + (SHARED ? 16 * s.w : 0);
+  const bool split = !SHARED && p.split_k;
+  const int64_t n0 = (int64_t)tile * (split ? 16 : 64) + (split ? 0 : 16 * s.w);
   s.set_weight(p.w1, p.s1, rec.e, p.N1, n0);
-  s.set_rows(rec.n, [&](int r) { return (uint32_t)(2 * tok[r] * p.D); });
+  s.set_rows(rec.n, [&](int r) {
+    const int t = SHARED ? tok[r] : (tokens & 1) ? r : 1;
+    return (uint32_t)(2 * t * p.D);
+  });
   const int c = 4 * s.q;
   v4f chan = {1.f, 1.f, 1.f, 1.f};
   if constexpr (WF == WF_INT8) {
@@ -448,7 +534,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
     for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(chan[k]));
   }
   const int units = (int)s.units;
-  const int lo = SHARED ? 0 : s.w * units / EXP_WAVES, hi = SHARED ? units : (s.w + 1) * units / EXP_WAVES;
+  const int lo = split ? s.w * units / EXP_WAVES : 0, hi = split ? (s.w + 1) * units / EXP_WAVES : units;
 #pragma unroll
   for (int k = 0; k < U - 1; ++k) s.issue(k, lo + k, lo + k < hi);
   v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -460,7 +546,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
     sl = sl == U - 1 ? 0 : sl + 1;
   }
   wait_vmem_le<0>();                           // no DMA into LDS that is used for something else
-  if constexpr (!SHARED) {
+  if (split) {
     __syncthreads();
     sm.part[s.w][s.lane] = acc;
     __syncthreads();

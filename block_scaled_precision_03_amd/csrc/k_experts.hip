@@ -135,18 +135,20 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   a.topk = topk;
   a.act = activation;
   const bool few = T <= f.private_t;
-  const int rows = few ? 16 : 16 * EXP_WAVES;
-  a.up_tiles = (int)cdiv(a.N1, rows);
-  a.down_tiles = (int)cdiv(D, rows);
+  const int64_t P = T * topk, live = std::min<int64_t>(E, P);
+  // One or two tokens: 64 rows of W1 per workgroup where that makes two per
+  // compute unit, else 16 with K split over the waves.
+  a.split_k = few && live * cdiv(a.N1, 64) < 2 * cu_count();
+  a.up_tiles = (int)cdiv(a.N1, a.split_k ? 16 : 64);
+  a.down_tiles = (int)cdiv(D, few ? 16 : 64);
   // Few columns leave compute units idle: the records are split over several
   // workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds their sums).
   a.splits = few ? 1 : (int)std::max<int64_t>(1, EXP_SPLIT_BLOCKS / a.down_tiles);
-  // records: experts with tokens, and one more per 16 tokens of an expert
-  const int64_t P = T * topk, live = std::min<int64_t>(E, P);
   // Up to 5 tokens per expert that has any: records of 8, whose smaller
   // stages leave room for more of them in flight; else 16 (an expert of more
   // tokens than that is read again).
   a.rows = P <= 5 * live ? 8 : EXP_ROWS;
+  // records: experts with tokens, and one more per `rows` tokens of an expert
   const int64_t most = live + (P - live) / a.rows;
   // F = 0: no tiles, no list; neither weights nor scales (which may be null) are touched
   const unsigned up = (unsigned)(1 + most * a.up_tiles), down = (unsigned)(a.down_tiles * a.splits);
