@@ -741,6 +741,32 @@ struct DenseLoop {
     }
   }
 
+  // All of a finished tile.  With a residual this is done between two tiles'
+  // steps: its loads and the stores share one counter, in order, so that spread
+  // over the next step each row tile's residual would wait for the stores
+  // of the row tile before it, and to load it whole the step has no registers left
+  // (16384 x 4096 x 4096: 267 us with MXFP8, 217 with the bias alone).  The next tile's
+  // first stage is already on its way.
+  __device__ static inline void finish_tile(const Ctx &c, const Epi &e, const v4f (&acc)[FM][FN]) {
+    // As many row tiles' residuals at once as registers allow; a later one's
+    // loads are behind the stores of row tiles finished long before its turn.
+    constexpr int WIN = FUSE != FUSE_RES_ACT ? FM : FP4 || (MX && !PSB) ? 3 : 4;
+    ResRow res[WIN];
+    if constexpr (RES) {
+      if (e.full) {
+#pragma unroll
+        for (int a = 0; a < WIN; ++a) load_residual(c, e, a, res[a]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      store_rows(c, e, a, acc[a], res[a % WIN]);
+      if constexpr (RES) {
+        if (e.full && a + WIN < FM) load_residual(c, e, a + WIN, res[a % WIN]);
+      }
+    }
+  }
+
   // One K step from ring slot si (scale slot gs).  With EPI the step is the
   // first of a tile: each accumulator row a-tile is first handed to the
   // epilogue `e` (the previous tile's result, stored while the matrix cores
@@ -788,12 +814,6 @@ struct DenseLoop {
       }
       return E8M0_ONE_X4;
     };
-    // The residual of a row tile is loaded while the row tile before it is
-    // finished.
-    ResRow res[2];
-    if constexpr (EPI && RES) {
-      if (e.on && e.full) load_residual(c, e, 0, res[0]);
-    }
     // A stage of two K steps (FP4) reads both steps' B fragments and scales
     // up front, so that the second step's reads overlap the first step's
     // matrix work instead of stalling between the two (not in the first step
@@ -871,7 +891,7 @@ struct DenseLoop {
             scp[a & 1] = __uint_as_float(saw[a]) * wsv;
             // the previous tile's rows leave before this tile's partials
             // replace them (one row tile later)
-            if (EPI && s == 0 && e.on) store_rows(c, e, a, acc[a], res[0]);
+            if (EPI && s == 0 && e.on) store_rows(c, e, a, acc[a], ResRow{});
 #pragma unroll
             for (int b = 0; b < FN; ++b)
               part[a & 1][b] = mfma_scaled<FB, FA>(bf[b], af, zero, E8M0_ONE_X4, E8M0_ONE_X4);
@@ -924,11 +944,8 @@ struct DenseLoop {
         int sa = E8M0_ONE_X4;
         if constexpr (MX) sa = (int)((SA_AHEAD ? saw[0] : saw[a]) >> (8 * c.q));
         if (EPI && s == 0) {
-          if (e.on) {
-            if constexpr (RES) {
-              if (e.full && a + 1 < FM) load_residual(c, e, a + 1, res[(a + 1) & 1]);
-            }
-            store_rows(c, e, a, acc[a], res[a & 1]);
+          if constexpr (!RES) {
+            if (e.on) store_rows(c, e, a, acc[a], ResRow{});
           }
 #pragma unroll
           for (int b = 0; b < FN; ++b) {
@@ -1032,7 +1049,7 @@ struct DenseLoop {
         // This wave's part of the next stage has landed (and, with no
         // epilogue in flight, everything else); the barrier publishes every
         // wave's DMA.
-        if (EPI && e.on && e.full) wait_vmem_le<EPI_STORES>();
+        if (!RES && EPI && e.on && e.full) wait_vmem_le<EPI_STORES>();
         else wait_vmem_le<0>();
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -1044,8 +1061,10 @@ struct DenseLoop {
         step(std::false_type{}, std::integral_constant<int, 0>{}, k + 1);
       }
       if (k < nst) step(std::false_type{}, std::integral_constant<int, 1>{}, k);
-      // this tile's result goes out during the next tile's first step
+      // this tile's result goes out during the next tile's first step; with a
+      // residual here, see finish_tile
       make_epi(c, cur.m0, cur.n0, cur.lim, alpha, true, e, cur.bslot);
+      if constexpr (RES) finish_tile(c, e, acc);
       if (more) {
         set_tile(c, resolve(tm, tn), cur);
         cur.bslot = (t + 1) & 1;
@@ -1057,15 +1076,7 @@ struct DenseLoop {
         }
       }
     }
-    ResRow res[FM];
-    if constexpr (RES) {
-      if (e.full) {
-#pragma unroll
-        for (int a = 0; a < FM; ++a) load_residual(c, e, a, res[a]);
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a], res[a]);
+    if constexpr (!RES) finish_tile(c, e, acc);
   }
 };
 

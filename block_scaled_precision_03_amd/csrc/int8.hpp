@@ -401,6 +401,28 @@ struct Int8Loop {
     }
   }
 
+  // All of a finished tile; with a residual between two tiles' steps (see
+  // DenseLoop::finish_tile).
+  __device__ static inline void finish_tile(const Ctx &c, const Epi &e, const v4i (&acc)[FM][FN]) {
+    // As many row tiles' residuals at once as registers allow; a later one's
+    // loads are behind the stores of row tiles finished long before its turn.
+    constexpr int WIN = SWIGLU ? FM : 5;
+    ResRow res[WIN];
+    if constexpr (RES) {
+      if (e.full) {
+#pragma unroll
+        for (int a = 0; a < WIN; ++a) load_residual(c, e, a, res[a]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      store_rows(c, e, a, acc[a], res[a % WIN]);
+      if constexpr (RES) {
+        if (e.full && a + WIN < FM) load_residual(c, e, a + WIN, res[a % WIN]);
+      }
+    }
+  }
+
   __device__ static inline void pin(v4i (&acc)[FM][FN]) {
 #pragma unroll
     for (int a = 0; a < FM; ++a)
@@ -418,11 +440,6 @@ struct Int8Loop {
       b1[b] = lds_read16(base + ob1 + b * 2048);
     }
     v4i a0 = lds_read16(base + oa0), a1 = lds_read16(base + oa1);
-    // the residual of a row tile is loaded while the one before it is finished
-    ResRow res[2];
-    if constexpr (EPI && RES) {
-      if (e.on && e.full) load_residual(c, e, 0, res[0]);
-    }
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
       v4i n0, n1;
@@ -430,12 +447,7 @@ struct Int8Loop {
         n0 = lds_read16(base + oa0 + (a + 1) * 2048);
         n1 = lds_read16(base + oa1 + (a + 1) * 2048);
       }
-      if (EPI && e.on) {
-        if constexpr (RES) {
-          if (e.full && a + 1 < FM) load_residual(c, e, a + 1, res[(a + 1) & 1]);
-        }
-        store_rows(c, e, a, acc[a], res[a & 1]);
-      }
+      if (!RES && EPI && e.on) store_rows(c, e, a, acc[a], ResRow{});
       // first operand = B tile: the result lane holds 4 consecutive n
 #pragma unroll
       for (int b = 0; b < FN; ++b) acc[a][b] = mfma_i8(b0[b], a0, EPI ? (v4i){0, 0, 0, 0} : acc[a][b]);
@@ -497,7 +509,7 @@ struct Int8Loop {
         compute<EPI>(c, smem, SC, oa0, oa1, ob0, ob1, acc, e);
         pin(acc);
         __builtin_amdgcn_sched_barrier(0);
-        if (EPI && e.on && e.full) wait_vmem_le<EPI_STORES>();
+        if (!RES && EPI && e.on && e.full) wait_vmem_le<EPI_STORES>();
         else wait_vmem_le<0>();
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -510,6 +522,7 @@ struct Int8Loop {
       }
       if (k < nst) step(std::false_type{}, std::integral_constant<int, 1>{}, k);
       make_epi(c, cur, true, e);
+      if constexpr (RES) finish_tile(c, e, acc);
       if (more) {
         set_tile(c, resolve(tm, tn), (t + 1) & 1, cur);
         if (odd) {
@@ -519,15 +532,7 @@ struct Int8Loop {
         }
       }
     }
-    ResRow res[FM];
-    if constexpr (RES) {
-      if (e.full) {
-#pragma unroll
-        for (int a = 0; a < FM; ++a) load_residual(c, e, a, res[a]);
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < FM; ++a) store_rows(c, e, a, acc[a], res[a]);
+    if constexpr (!RES) finish_tile(c, e, acc);
   }
 };
 
