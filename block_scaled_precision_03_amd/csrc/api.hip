@@ -154,19 +154,47 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
 }
 
 // Kernel choice of the residual epilogue: those of mxgemm_dense_variant, and
-// the kernels for few rows.
+// the kernels for few rows (rows.hpp) by estimated times from static shapes,
+// fitted to 200 calls of 1 .. 400 rows (N 128 .. 16000, K 256 .. 15360, MXFP8 and
+// MXFP4, plain and preshuffled B, cold weights), every kernel timed on each: 2 %
+// over the fastest on average, over 14 % in 10 of them, at most 46 %.  Both sides where the
+// choice turns, in us: 1 x 4096 x 14336 FP8 17 in 16 x 16 tiles, 30 in 32 x 32, 94 in the 64 x 64
+// kernel; 45 x 6200 x 8448 preshuffled 31, 30, 22 in 64 x 32 and 45; 163 x 2009 x 512
+// 10.5, 8.8, 6.7 and 10.8; 15336 columns of 256 x 7 rows FP4 4.9, 4.2, 5.9 and 4.4.
 namespace {
-// Row tiles of the kernels for few rows: 16, 32 or 64 rows.
-int rows_fm(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
-
-bool few_rows(int fmtA, int64_t M, int64_t N, int64_t K) {
-  return M <= 64;
+// The row tiles of the few-row kernel that is fastest (16 fm rows), 0: another kernel.
+int rows_fm(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
+  if (layout != MXG_NT || M <= 0 || M > 1024 || N <= 0 || K < 128 || fmtA == MXG_INT8) return 0;
+  const bool psb = (fmtB & MXG_PRESHUFFLED) != 0, fp4 = fmtA == MXG_MXFP4_E2M1;
+  const double cus = cu_count(), nst = (double)(K / 128), kb = fp4 ? 0.5 * K : (double)K;
+  const double bytes = (double)N * kb + (double)M * kb + 4.0 * (double)M * (double)N;
+  // start, a compute unit's operand bytes per us, all memory's, a tile's end
+  struct { double t0, rate, mem, tile; } model[2][3] = {
+      {{3.23, 23.1e3, 3.98e6, 0.38}, {3.16, 20.9e3, 3.16e6, 1.03}, {3.39, 19.2e3, 2.69e6, 1.58}},
+      {{3.32, 36.5e3, 6.28e6, 0.59}, {3.05, 34.8e3, 4.37e6, 1.90}, {3.25, 27.6e3, 3.60e6, 2.45}}};
+  int best = 0;
+  // the 64 x 64 kernel as timed there; the 256 x 256 one as mxgemm_dense_variant has it
+  const double t64[2][2][3] = {{{4.08, 0.914, 2.14}, {3.55, 0.554, 2.71}}, {{3.99, 0.523, 2.46}, {3.67, 0.361, 2.95}}};
+  const double *s = t64[psb][fp4], n64 = (double)(cdiv(M, SBM) * cdiv(N, SBN));
+  double least = s[0] + std::ceil(n64 / cus) * s[1] * nst + s[2] * n64 / cus;
+  least = std::min(least, 6.0 + std::ceil((double)(cdiv(M, DBM) * cdiv(N, DBN)) / cus) * 1.3 * nst);
+  for (int i = 0; i < 3; ++i) {
+    const int bm = 16 << i, bn = i == 0 ? 16 : 32;
+    const int64_t tm = cdiv(M, bm);
+    const double n = (double)(tm * cdiv(N, bn)), ops = (std::min((double)bm, (double)M / tm) + bn) * kb;
+    const auto &m = model[psb][i];
+    const double t = m.t0 + std::max(std::max(1.0, n / cus) * ops / m.rate, bytes / m.mem) + m.tile * n / cus;
+    if (t < least) {
+      least = t;
+      best = 1 << i;
+    }
+  }
+  return best;
 }
 }  // namespace
 
 extern "C" int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  if (layout == MXG_NT && M > 0 && N > 0 && K > 0 && fmtA != MXG_INT8 && few_rows(fmtA, M, N, K)) return MXG_DENSE_ROWS;
-  return mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+  return rows_fm(fmtA, fmtB, layout, M, N, K) ? MXG_DENSE_ROWS : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
 }
 
 namespace {
@@ -224,10 +252,9 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   }
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  const int variant = fuse >= FUSE_RES ? mxgemm_residual_variant(fmtA, fmtB, layout, M, N, K)
-                                       : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
-  const bool small = variant == MXG_DENSE_TILE64, rows = variant == MXG_DENSE_ROWS;
-  const int fm = rows_fm(M);
+  const int fm = fuse >= FUSE_RES ? rows_fm(fmtA, fmtB, layout, M, N, K) : 0;
+  const bool rows = fm > 0;
+  const bool small = !rows && mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64;
   dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, fm)
                 : small ? pick_small(fa.elem, fb.elem, fa.mx, psb, fuse)
                         : pick_dense(fa.elem, fb.elem, fa.mx, layout, psb, fuse);

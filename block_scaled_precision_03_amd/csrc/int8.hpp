@@ -95,60 +95,62 @@ __device__ inline void int8_store4(const Int8Args &p, int act, int64_t row, int6
   }
 }
 
-// N values of a BF16 row of which `room` are left, at any alignment.
-template <int N>
-__device__ inline void load_bf16_any(const uint16_t *src, int64_t room, float (&v)[N]) {
-  uint16_t h[N];
-  if (room >= N) {
-    __builtin_memcpy(h, src, 2 * N);
-  } else {
+// The residual beside four consecutive columns of the product (SwiGLU: two of
+// D), packed, at any alignment; zeros past the row's end and without one.
+__device__ inline v2i int8_near(const Int8Args &p, int act, int64_t row, int64_t col) {
+  uint32_t u[2] = {0, 0};
+  if (p.R) {
+    const bool gated = act == ACT_SWIGLU;
+    const int64_t oc = gated ? col >> 1 : col, room = p.No - oc;
+    const uint16_t *src = p.R + row * p.No + oc;
+    if (gated && room >= 2) {
+      __builtin_memcpy(u, src, 4);
+    } else if (!gated && room >= 4) {
+      __builtin_memcpy(u, src, 8);
+    } else {
 #pragma unroll
-    for (int k = 0; k < N; ++k) h[k] = k < room ? src[k] : (uint16_t)0;
+      for (int k = 0; k < 4; ++k)
+        if (k < room && (k < 2 || !gated)) u[k >> 1] |= (uint32_t)src[k] << (16 * (k & 1));
+    }
   }
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = __uint_as_float((uint32_t)h[k] << 16);
-}
-template <int N>
-__device__ inline void store_bf16_any(uint16_t *dst, int64_t room, const float (&v)[N]) {
-  uint32_t u[N / 2];
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) u[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-  if (room >= N) {
-    __builtin_memcpy(dst, u, 2 * N);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (k < room) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
-  }
+  return (v2i){(int)u[0], (int)u[1]};
 }
 
 // Four consecutive columns of the product, scaled and biased but not
 // activated, to what the call returns; RES: the activation's argument too,
 // and the residual added.
 template <bool RES>
-__device__ inline void int8_emit4(const Int8Args &p, int act, int64_t row, int64_t col, v4f z) {
-  if constexpr (!RES) {
+__device__ inline void int8_emit4(const Int8Args &p, int act, int64_t row, int64_t col, v4f z, const v2i &near) {
+  if constexpr (RES) {
+    if (p.Z) {
+      uint16_t *dst = p.Z + row * p.N + col;
+      const uint32_t u[2] = {pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w)};
+      if (col + 4 <= p.N) {
+        __builtin_memcpy(dst, u, 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (col + k < p.N) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
+      }
+    }
+    const v4f r = unpack_bf16x4(near);
+    if (act == ACT_SWIGLU) {
+      const int64_t oc = col >> 1;
+      uint16_t *dst = p.D + row * p.No + oc;
+      const uint32_t u = pack_bf16x2(z.x * logistic_f32(z.x) * z.y + r.x, z.z * logistic_f32(z.z) * z.w + r.y);
+      if (oc + 2 <= p.No) __builtin_memcpy(dst, &u, 4);
+      else if (oc < p.No) dst[0] = (uint16_t)u;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = activate(act, z[k]) + r[k];
+    int8_store4(p, ACT_NONE, row, col, z);
+  } else {
     if (act != ACT_NONE && act != ACT_SWIGLU) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[k] = activate(act, z[k]);
     }
     int8_store4(p, act, row, col, z);
-  } else {
-    if (p.Z) store_bf16_any<4>(p.Z + row * p.N + col, p.N - col, {z.x, z.y, z.z, z.w});
-    if (act == ACT_SWIGLU) {
-      const int64_t oc = col >> 1;
-      float r[2] = {0.f, 0.f};
-      if (p.R) load_bf16_any<2>(p.R + row * p.No + oc, p.No - oc, r);
-      const float v[2] = {z.x * logistic_f32(z.x) * z.y + r[0], z.z * logistic_f32(z.z) * z.w + r[1]};
-      store_bf16_any<2>(p.D + row * p.No + oc, p.No - oc, v);
-    } else {
-      float r[4] = {0.f, 0.f, 0.f, 0.f};
-      if (p.R) load_bf16_any<4>(p.R + row * p.No + col, p.No - col, r);
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = activate(act, z[k]) + r[k];
-      store_bf16_any<4>(p.D + row * p.No + col, p.No - col, v);
-    }
   }
 }
 
@@ -394,7 +396,7 @@ struct Int8Loop {
 #pragma unroll
         for (int b = 0; b < FN; ++b) {
           const int64_t col = e.n0 + c.wn * (FN * 16) + b * 16 + 4 * q;
-          if constexpr (RES) int8_emit4<true>(p, ACT, r, col, finish(b));
+          if constexpr (RES) int8_emit4<true>(p, ACT, r, col, finish(b), int8_near(p, ACT, r, col));
           else int8_store4(p, ACT, r, col, finish(b));
         }
       }
@@ -711,6 +713,17 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
       bias[b] = unpack_bf16x4(u);
     }
     const int64_t r0 = t.row0 + wm * (BM / 2) + i16;
+    // all of the residual before the first store: their latencies together
+    v2i near[RES ? FM : 1][FN];
+    if constexpr (RES) {
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b) {
+          near[a][b] = (v2i){0, 0};
+          if (r0 + a * 16 < t.lim) near[a][b] = int8_near(p, ACT, r0 + a * 16, t.n0 + wn * (BN / 2) + b * 16 + 4 * q);
+        }
+    }
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
       const float sa = __uint_as_float(*(const lds_u32_t *)(uintptr_t)(sc + (uint32_t)(4 * (wm * (BM / 2) + a * 16 + i16))));
@@ -718,7 +731,7 @@ __global__ __launch_bounds__(256, 2) void int8_stream_kernel(Int8Args p) {
 #pragma unroll
         for (int b = 0; b < FN; ++b)
           int8_emit4<RES>(p, ACT, r0 + a * 16, t.n0 + wn * (BN / 2) + b * 16 + 4 * q,
-                          int8_finish(acc[a][b], sa, sb[b], bias[b], ACT_NONE));
+                          int8_finish(acc[a][b], sa, sb[b], bias[b], ACT_NONE), near[RES ? a : 0][b]);
       }
     }
   };
@@ -887,9 +900,11 @@ __global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args p) {
     for (int k = 1; k < W; ++k) sum += part[k][f][lane];
     const int64_t row = t.row0 + 16 * a + i16, col = t.n0 + 16 * b + 4 * q;
     if (row < t.lim) {
+      v2i near = {0, 0};
+      if constexpr (RES) near = int8_near(p, p.act, row, col);
       v4f sb, bias;
       int8_columns(p, t.g, t.n0, 16 * b + 4 * q, sb, bias);
-      int8_emit4<RES>(p, p.act, row, col, int8_finish(sum, p.sA[row], sb, bias, ACT_NONE));
+      int8_emit4<RES>(p, p.act, row, col, int8_finish(sum, p.sA[row], sb, bias, ACT_NONE), near);
     }
   }
 }

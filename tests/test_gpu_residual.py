@@ -117,6 +117,25 @@ def test_small_outputs(name, M, N, K):
     Case(name, M, N, k_of(name, K), a=ACTS[M % 4], seed=M).check()
 
 
+@pytest.mark.parametrize("name", ["mx44", "fp4", "tw54", "mx45"])
+@pytest.mark.parametrize("psb", [False, True])
+@pytest.mark.parametrize("M,N,K,fm", [(3, 70, 1024, "ROWS"), (40, 2050, 2048, "ROWS"), (100, 3000, 2048, "ROWS"), (19, 8200, 256, None),
+                                      (700, 770, 512, None), (4, 40000, 256, None), (300, 6000, 256, None)])
+def test_every_kernel(name, psb, M, N, K, fm):
+    m = _mx()
+    fa, fb = FORMATS[name]
+    if fm:
+        assert m.residual_variant(fa, fb | (m.PRESHUFFLED if psb else 0), m.NT, M, N, K) == m.DENSE_ROWS
+    Case(name, M, N, K, a=R.ACT_SILU, psb=psb, seed=M).check()
+
+
+def test_every_kernel_is_chosen_somewhere():
+    m = _mx()
+    sizes = [(3, 70, 1024), (19, 8200, 256), (700, 770, 512), (4, 40000, 256), (300, 6000, 256), (2148, 2304, 512)]
+    got = {m.residual_variant(f, f, m.NT, *s) for f in (0, 4, 16) for s in sizes}
+    assert got == {m.DENSE_ROWS, m.DENSE_TILE64, m.DENSE_TILE256}
+
+
 @pytest.mark.parametrize("name", ["mx44", "fp4", "tw54", "mx54"])
 @pytest.mark.parametrize("M,N", [(1, 130), (9, 4098), (65, 200)])
 def test_preshuffled(name, M, N):
@@ -262,7 +281,7 @@ ALL = ACTS + [R.ACT_SWIGLU]
 
 
 @pytest.mark.parametrize("a", ALL)
-@pytest.mark.parametrize("M,N", [(1, 2), (1, 1000), (2, 8), (15, 514), (16, 512), (17, 510), (129, 5002), (300, 4608), (2000, 66)])
+@pytest.mark.parametrize("M,N", [(1, 2), (1, 1000), (2, 8), (15, 514), (16, 512), (17, 510), (129, 5002), (256, 258), (257, 260), (300, 4608), (2000, 66)])
 def test_gradient(a, M, N):
     backward(a, M, N, seed=M, special=M * N > 100)
 

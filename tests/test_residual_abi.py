@@ -41,11 +41,11 @@ BACKWARD = [((0, P, 0, 0, Q, 64, 66, P), 0), ((0, P, 0, Q, 0, 64, 66, None), 0),
             ((2, P, Q, P, 0, 64, 66, None), 0), ((8, P, Q, Q, P, 64, 66, P), 0), ((1, P, Q, S, P, 8, 65, None), 0),
             ((1, 0, 0, 0, P, 0, 65, None), 0), ((1, 0, 0, 0, P, 64, 0, None), 0),
             ((4, P, Q, S, 0, 64, 66, None), -1), ((-1, P, Q, S, 0, 64, 66, None), -1), ((1, P, Q, 0, 0, 64, 66, None), -1),
-            ((1, 0, Q, S, 0, 64, 66, None), -1), ((1, P, 0, S, 0, 64, 66, None), -1), ((1, P, Q, S, P, 64, 66, None), -1),
+            ((1, 0, Q, S, 0, 64, 66, None), -1), ((1, P, 0, S, 0, 64, 66, None), -1), ((1, P, Q, S, P, 300, 66, None), -1),
             ((8, P, Q, P, 0, 64, 66, None), -1), ((1, P, Q, S, 0, -1, 66, None), -1), ((1, P, Q, S, 0, 64, -2, None), -1),
             ((8, P, Q, S, 0, 64, 65, None), -2), ((1, P, Q, S, 0, 1 << 31, 2, None), -2), ((1, P, Q, S, 0, 2, 1 << 31, None), -2),
             ((1, P + 2, Q, S, 0, 64, 66, None), -3), ((1, P, Q + 8, S, 0, 64, 66, None), -3), ((1, P, Q, S + 4, 0, 64, 66, None), -3),
-            ((1, P, Q, S, P + 2, 64, 66, P), -3), ((1, P, Q, S, P, 64, 66, P + 8), -3)]
+            ((1, P, Q, S, P + 2, 64, 66, P), -3), ((1, P, Q, S, P, 300, 66, P + 8), -3), ((1, P, Q, S, P, 64, 66, None), 0)]
 
 
 @pytest.mark.parametrize("args,status", BACKWARD)
@@ -62,12 +62,13 @@ def test_backward_workspace():
     m = _mx()
     assert m.residual_backward_workspace_bytes(0, 5) == 0 and m.residual_backward_workspace_bytes(1, 5) == 0
     assert m.residual_backward_workspace_bytes(-1, 5) == -1 and m.residual_backward_workspace_bytes(5, 1 << 31) == -1
-    need = m.residual_backward_workspace_bytes(64, 66)
+    assert m.residual_backward_workspace_bytes(256, 66) == 0           # one part
+    need = m.residual_backward_workspace_bytes(300, 66)
     assert need > 0 and need % (4 * 66) == 0
     room = torch.empty(need + 32, dtype=torch.uint8)
     start = -room.data_ptr() % 16
-    assert m.residual_backward_validate(1, P, Q, S, P, 64, 66, workspace=room[start:start + need]) == 0
-    assert m.residual_backward_validate(1, P, Q, S, P, 64, 66, workspace=room[start:start + need - 1]) == -1
+    assert m.residual_backward_validate(1, P, Q, S, P, 300, 66, workspace=room[start:start + need]) == 0
+    assert m.residual_backward_validate(1, P, Q, S, P, 300, 66, workspace=room[start:start + need - 1]) == -1
 
 
 @pytest.mark.parametrize("a", [R.ACT_NONE, R.ACT_RELU, R.ACT_GELU, R.ACT_SILU, R.ACT_SWIGLU])
