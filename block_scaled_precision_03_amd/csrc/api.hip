@@ -19,7 +19,6 @@
 #include "kernels.hpp"
 #include "preshuffle.hpp"
 #include "quant.hpp"
-#include "rows.hpp"
 #include "diag.hpp"
 
 using namespace mxg;
@@ -154,39 +153,43 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
 }
 
 // Kernel choice of the residual epilogue: those of mxgemm_dense_variant, and
-// the kernels for few rows (rows.hpp) by estimated times from static shapes,
-// fitted to 200 calls of 1 .. 400 rows (N 128 .. 16000, K 256 .. 15360, MXFP8 and
-// MXFP4, plain and preshuffled B, cold weights), every kernel timed on each: 2 %
-// over the fastest on average, over 14 % in 10 of them, at most 46 %.  Both sides where the
-// choice turns, in us: 1 x 4096 x 14336 FP8 17 in 16 x 16 tiles, 30 in 32 x 32, 94 in the 64 x 64
-// kernel; 45 x 6200 x 8448 preshuffled 31, 30, 22 in 64 x 32 and 45; 163 x 2009 x 512
-// 10.5, 8.8, 6.7 and 10.8; 15336 columns of 256 x 7 rows FP4 4.9, 4.2, 5.9 and 4.4.
+// the kernels for few rows or columns (rows.hpp) by estimated times from static
+// shapes, fitted to 250 calls of 1 .. 400 rows (N 128 .. 16000, K 256 .. 15360, MXFP8
+// and MXFP4, plain and preshuffled B, cold weights), every kernel timed on each:
+// 1 % over the fastest on average, over 14 % in 5 of them, at most 27 %.  Both sides where the
+// choice turns, in us (8 x 16, 16 x 16, 32 x 32, 64 x 32, 64 x 64 tiles; the 64 x 64 kernel of
+// small.hpp): 16 x 8192 x 8192 FP8 25, 18.4, 16.5, 17.1, 24.7; 64; 17 x 2796 x 1792 7.9, 7.6, 5.6,
+// 6.5, 8.2; 14.7; 44 x 8461 x 2048 -, 27, 17.1, 14.5, 10.9; 25.9; 4 x 14096 x 256 FP4 6.0, 10.6, 6.7,
+// 7.4, 4.9; 4.0.
 namespace {
-// The row tiles of the few-row kernel that is fastest (16 fm rows), 0: another kernel.
-int rows_fm(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  if (layout != MXG_NT || M <= 0 || M > 1024 || N <= 0 || K < 128 || fmtA == MXG_INT8) return 0;
+// The tile of the kernel for few rows that is fastest, -1: another kernel.
+int rows_tile(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
+  if (layout != MXG_NT || M <= 0 || M > 512 || N <= 0 || K < 128 || fmtA == MXG_INT8) return -1;
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0, fp4 = fmtA == MXG_MXFP4_E2M1;
   const double cus = cu_count(), nst = (double)(K / 128), kb = fp4 ? 0.5 * K : (double)K;
   const double bytes = (double)N * kb + (double)M * kb + 4.0 * (double)M * (double)N;
-  // start, a compute unit's operand bytes per us, all memory's, a tile's end
-  struct { double t0, rate, mem, tile; } model[2][3] = {
-      {{3.23, 23.1e3, 3.98e6, 0.38}, {3.16, 20.9e3, 3.16e6, 1.03}, {3.39, 19.2e3, 2.69e6, 1.58}},
-      {{3.32, 36.5e3, 6.28e6, 0.59}, {3.05, 34.8e3, 4.37e6, 1.90}, {3.25, 27.6e3, 3.60e6, 2.45}}};
-  int best = 0;
+  // start; a tile's own time; a compute unit's operand bytes and all memory's per us
+  struct Model { double t0, tile, rate, mem; };
+  const Model model[2][ROWS_TILE_COUNT] = {
+      {{2.15, 1.46, 43.2e3, 5.45e6}, {1.52, 2.41, 50.3e3, 4.65e6}, {1.03, 2.92, 48.3e3, 3.73e6}, {1.31, 3.24, 42.5e3, 3.46e6}, {0.0, 4.97, 42.0e3, 2.82e6}},
+      {{2.39, 1.24, 42.5e3, 5.24e6}, {1.61, 2.47, 65.2e3, 4.36e6}, {1.14, 3.05, 53.7e3, 3.98e6}, {1.34, 3.63, 49.2e3, 3.27e6}, {0.0, 5.61, 45.6e3, 3.29e6}}};
   // the 64 x 64 kernel as timed there; the 256 x 256 one as mxgemm_dense_variant has it
-  const double t64[2][2][3] = {{{4.08, 0.914, 2.14}, {3.55, 0.554, 2.71}}, {{3.99, 0.523, 2.46}, {3.67, 0.361, 2.95}}};
+  const double t64[2][2][3] = {{{3.77, 0.943, 1.89}, {3.82, 0.555, 2.48}}, {{3.73, 0.523, 2.82}, {4.13, 0.340, 2.89}}};
   const double *s = t64[psb][fp4], n64 = (double)(cdiv(M, SBM) * cdiv(N, SBN));
   double least = s[0] + std::ceil(n64 / cus) * s[1] * nst + s[2] * n64 / cus;
   least = std::min(least, 6.0 + std::ceil((double)(cdiv(M, DBM) * cdiv(N, DBN)) / cus) * 1.3 * nst);
-  for (int i = 0; i < 3; ++i) {
-    const int bm = 16 << i, bn = i == 0 ? 16 : 32;
-    const int64_t tm = cdiv(M, bm);
-    const double n = (double)(tm * cdiv(N, bn)), ops = (std::min((double)bm, (double)M / tm) + bn) * kb;
-    const auto &m = model[psb][i];
-    const double t = m.t0 + std::max(std::max(1.0, n / cus) * ops / m.rate, bytes / m.mem) + m.tile * n / cus;
-    if (t < least) {
-      least = t;
-      best = 1 << i;
+  int best = -1;
+  for (int i = 0; i < ROWS_TILE_COUNT; ++i) {
+    const RowsTile &t = ROWS_TILES[i];
+    const Model &m = model[psb][i];
+    const int64_t tm = cdiv(M, t.rows);
+    const double n = (double)(tm * cdiv(N, t.cols)), ops = (std::min((double)t.rows, (double)M / tm) + t.cols) * kb;
+    // tiles per compute unit: whole rounds where one fills it
+    const double load = t.per_cu > 1 ? std::max(1.0, n / cus) : std::ceil(n / cus);
+    const double us = m.t0 + std::max(load * (m.tile + ops / m.rate), bytes / m.mem);
+    if (us < least) {
+      least = us;
+      best = i;
     }
   }
   return best;
@@ -194,7 +197,7 @@ int rows_fm(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
 }  // namespace
 
 extern "C" int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  return rows_fm(fmtA, fmtB, layout, M, N, K) ? MXG_DENSE_ROWS : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+  return rows_tile(fmtA, fmtB, layout, M, N, K) >= 0 ? MXG_DENSE_ROWS : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
 }
 
 namespace {
@@ -252,10 +255,10 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   }
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  const int fm = fuse >= FUSE_RES ? rows_fm(fmtA, fmtB, layout, M, N, K) : 0;
-  const bool rows = fm > 0;
+  const int tile = fuse >= FUSE_RES ? rows_tile(fmtA, fmtB, layout, M, N, K) : -1;
+  const bool rows = tile >= 0;
   const bool small = !rows && mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64;
-  dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, fm)
+  dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, tile)
                 : small ? pick_small(fa.elem, fb.elem, fa.mx, psb, fuse)
                         : pick_dense(fa.elem, fb.elem, fa.mx, layout, psb, fuse);
   if (!fn) return MXG_ERR_UNSUPPORTED;
@@ -273,8 +276,8 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   a.b_bytes = psb ? mxgemm_preshuffle_b_bytes(fmtB & ~MXG_PRESHUFFLED, N, K) : (fp4 ? N * K / 2 : N * K);
   a.sa_bytes = fa.mx ? M * (K / 32) : 4;
   a.sb_bytes = fb.mx ? (psb ? mxgemm_preshuffle_scales_bytes(N, K) : N * (K / 32)) : 4;
-  a.tiles_m = (int)cdiv(M, rows ? 16 * fm : small ? SBM : DBM);
-  a.tiles_n = (int)cdiv(N, rows ? (fm == 1 ? 16 : 32) : small ? SBN : DBN);
+  a.tiles_m = (int)cdiv(M, rows ? ROWS_TILES[tile].rows : small ? SBM : DBM);
+  a.tiles_n = (int)cdiv(N, rows ? ROWS_TILES[tile].cols : small ? SBN : DBN);
   a.bias = (const uint16_t *)bias;
   a.act = act;
   a.R = (const uint16_t *)residual;
@@ -282,7 +285,7 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   if (tiles > 0x7FFFFFFF) return MXG_ERR_UNSUPPORTED;
   if (rows) {
-    hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(64 * ROWS_WAVES), 0, stream, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3((unsigned)(64 * ROWS_TILES[tile].waves)), 0, stream, a);
     return launch_status();
   }
   if (small) {

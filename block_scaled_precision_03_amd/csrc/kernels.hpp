@@ -61,9 +61,14 @@ dense_fn pick_residual_tw_a5(int eb, bool psb, int fuse);
 dense_fn pick_residual_fp4(bool psb, int fuse);
 // k_small.hip: the 64 x 64 NT kernel, every format.
 dense_fn pick_small(int ea, int eb, bool mx, bool psb, int fuse);
-// k_rows.hip: 16 fm x 16 (fm 1) or 32 columns with K split over waves, fm 1, 2
-// or 4, residual epilogue.
-dense_fn pick_rows(int ea, int eb, bool mx, bool psb, int fm);
+// k_rows.hip: few rows or columns, residual epilogue, in these tiles: rows,
+// columns, waves, workgroups that a compute unit's LDS holds.
+struct RowsTile {
+  int rows, cols, waves, per_cu;
+};
+constexpr RowsTile ROWS_TILES[] = {{8, 16, 4, 2}, {16, 16, 8, 1}, {32, 32, 4, 1}, {64, 32, 4, 1}, {64, 64, 4, 1}};
+constexpr int ROWS_TILE_COUNT = 5;
+dense_fn pick_rows(int ea, int eb, bool mx, bool psb, int tile);
 // k_grouped.hip: the grouped kernels (256 x 256 dense pipeline; persistent
 // streaming with BM-row tiles; the streaming kernel on the dense pipeline's
 // tail pieces).

@@ -119,19 +119,23 @@ def test_small_outputs(name, M, N, K):
 
 @pytest.mark.parametrize("name", ["mx44", "fp4", "tw54", "mx45"])
 @pytest.mark.parametrize("psb", [False, True])
-@pytest.mark.parametrize("M,N,K,fm", [(3, 70, 1024, "ROWS"), (40, 2050, 2048, "ROWS"), (100, 3000, 2048, "ROWS"), (19, 8200, 256, None),
-                                      (700, 770, 512, None), (4, 40000, 256, None), (300, 6000, 256, None)])
-def test_every_kernel(name, psb, M, N, K, fm):
+@pytest.mark.parametrize("M,N,K,few", [(3, 70, 1024, True), (25, 1026, 2048, True),        # 8 x 16 tiles, one and several
+                                       (37, 1026, 2048, True), (13, 4098, 2048, None),       # 16 x 16
+                                       (16, 4098, 4096, True), (40, 2050, 2048, True),       # 32 x 32
+                                       (100, 3000, 2048, True), (60, 8194, 2048, True),      # 64 x 32, 64 x 64
+                                       (700, 770, 512, None), (4, 40000, 256, False), (300, 6000, 256, False)])
+def test_every_kernel(name, psb, M, N, K, few):
     m = _mx()
     fa, fb = FORMATS[name]
-    if fm:
-        assert m.residual_variant(fa, fb | (m.PRESHUFFLED if psb else 0), m.NT, M, N, K) == m.DENSE_ROWS
+    if few is not None:
+        got = m.residual_variant(fa, fb | (m.PRESHUFFLED if psb else 0), m.NT, M, N, K)
+        assert got == (m.DENSE_ROWS if few else m.DENSE_TILE64)
     Case(name, M, N, K, a=R.ACT_SILU, psb=psb, seed=M).check()
 
 
 def test_every_kernel_is_chosen_somewhere():
     m = _mx()
-    sizes = [(3, 70, 1024), (19, 8200, 256), (700, 770, 512), (4, 40000, 256), (300, 6000, 256), (2148, 2304, 512)]
+    sizes = [(3, 70, 1024), (100, 3000, 2048), (4, 40000, 256), (300, 6000, 256), (2148, 2304, 512)]
     got = {m.residual_variant(f, f, m.NT, *s) for f in (0, 4, 16) for s in sizes}
     assert got == {m.DENSE_ROWS, m.DENSE_TILE64, m.DENSE_TILE256}
 
