@@ -237,7 +237,7 @@ __global__ void bias_act_fill_kernel(uint16_t *D, int64_t M, int64_t N, const ui
 
 int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
               void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, const void *residual, void *z,
-              hipStream_t stream) {
+              bool few_rows, hipStream_t stream) {
   if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, residual, z, stream);
   const int fuse = residual != nullptr || z != nullptr        ? (act != MXG_ACT_NONE ? FUSE_RES_ACT : FUSE_RES)
                    : bias != nullptr || act != MXG_ACT_NONE ? FUSE_ACT
@@ -255,7 +255,7 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   }
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  const int tile = fuse >= FUSE_RES ? rows_tile(fmtA, fmtB, layout, M, N, K) : -1;
+  const int tile = few_rows ? rows_tile(fmtA, fmtB, layout, M, N, K) : -1;
   const bool rows = tile >= 0;
   const bool small = !rows && mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64;
   dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, tile)
@@ -304,7 +304,7 @@ extern "C" int mxgemm_run(int fmtA, int fmtB, int layout, const void *A, const v
                const void *sB, void *D, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int v = mxgemm_validate(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K);
   if (v != MXG_OK) return v;
-  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, nullptr, MXG_ACT_NONE, nullptr, nullptr, stream);
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, nullptr, MXG_ACT_NONE, nullptr, nullptr, false, stream);
 }
 
 extern "C" int mxgemm_validate_fused(int fmtA, int fmtB, int layout, const void *A, const void *sA,
@@ -331,7 +331,7 @@ extern "C" int mxgemm_run_fused(int fmtA, int fmtB, int layout, const void *A, c
                                 int activation, hipStream_t stream) {
   const int v = mxgemm_validate_fused(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation);
   if (v != MXG_OK) return v;
-  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, nullptr, nullptr, stream);
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, nullptr, nullptr, false, stream);
 }
 
 extern "C" int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B,
@@ -354,7 +354,7 @@ extern "C" int mxgemm_run_residual(int fmtA, int fmtB, int layout, const void *A
                                    int activation, const void *residual, void *z, hipStream_t stream) {
   const int v = mxgemm_validate_residual(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, residual, z);
   if (v != MXG_OK) return v;
-  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, residual, z, stream);
+  return run_dense(fmtA, fmtB, layout, A, sA, B, sB, D, M, N, K, bias, activation, residual, z, true, stream);
 }
 
 extern "C" int grouped_fp8_gemm_validate(int G, const int64_t *m_sizes, const void *XQ, const float *x_scale,

@@ -436,6 +436,8 @@ __device__ inline ExpertRec find_record(const SlotTable &s, int rank, uint64_t &
 __device__ inline void expert_table(const ExpertsArgs &p, const SlotTable &s) {
   const int lane = threadIdx.x & 63;
   const int base = __shfl(s.base, s.head);
+  for (int i = threadIdx.x; i < p.down_tiles; i += blockDim.x)
+    if (p.splits > 1) p.arrived[i] = 0;
   if (threadIdx.x >= 64) return;
   if (lane == 0) *p.count = __popcll(s.heads);
   if (s.heads >> lane & 1) p.rec[__popcll(s.heads & ((1ull << lane) - 1))] = ExpertRec{s.e, s.base, (int32_t)__popc(s.tokens), 0};
@@ -580,7 +582,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
   const RecPtr recs = (RecPtr)(uintptr_t)p.rec;
   const int units = (int)s.units;
   const int total = __builtin_amdgcn_readfirstlane(*p.count) * units;
-  const int pieces = SHARED ? p.splits : EXP_WAVES, mine = SHARED ? split : s.w;
+  const int pieces = SHARED ? p.splits : p.splits * EXP_WAVES, mine = SHARED ? split : split * EXP_WAVES + s.w;
   const int lo = (int)((int64_t)total * mine / pieces), hi = (int)((int64_t)total * (mine + 1) / pieces);
 
   // the stage to issue, and the one to use: record and unit
@@ -657,8 +659,12 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int t = t0 + j * GROUP;
-    if (in && t < p.T)
-      __builtin_amdgcn_raw_buffer_store_b128(*(const u4v *)&sums[0][t][c], rp, place(split, t, c), 0, DEVICE);
+    if (in && t < p.T) {
+      v4f v = *(const v4f *)&sums[0][t][c];
+#pragma unroll
+      for (int k = 1; k < SETS; ++k) v += *(const v4f *)&sums[k][t][c];
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v), rp, place(split, t, c), 0, DEVICE);
+    }
   }
   wait_vmem_le<0>();
   __syncthreads();
@@ -692,8 +698,8 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
     const int t = t0 + j * GROUP;
     if (t >= p.T) break;
     const int64_t o = (int64_t)t * p.D + tile0 + c;
-    if (p.residual) v[j] += load_bf16x4(p.residual + o, 4, true);
-    store_bf16x4(p.out + o, v[j], 4, true);
+    if (p.residual) v[j] += load_bf16x4(p.residual + o, 4);
+    store_bf16x4(p.out + o, v[j], 4);
   }
 }
 

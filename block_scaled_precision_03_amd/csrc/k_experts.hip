@@ -1,6 +1,7 @@
 // C ABI of the experts of a mixture-of-experts layer for a few tokens:
 // argument checks and launch.
 #include <algorithm>
+#include <cmath>
 
 #include "experts.hpp"
 #include "host.hpp"
@@ -18,15 +19,16 @@ struct ExpertsFormat {
   int64_t unit;
   bool scales;
   int private_t;
+  int64_t (*row_bytes)(int64_t);
 };
 bool experts_format(int fmt, ExpertsFormat &f) {
   switch (fmt) {
-    case MXG_INT8: f = {WF_INT8, 16, true, WeightFormat<WF_INT8>::PRIVATE_T}; return true;
-    case MXG_BF16: f = {WF_BF16, 8, false, WeightFormat<WF_BF16>::PRIVATE_T}; return true;
-    case MXG_MXFP8_E4M3: f = {WF_E4M3, 32, true, WeightFormat<WF_E4M3>::PRIVATE_T}; return true;
-    case MXG_MXFP8_E5M2: f = {WF_E5M2, 32, true, WeightFormat<WF_E5M2>::PRIVATE_T}; return true;
-    case MXG_MXFP4_E2M1: f = {WF_E2M1, 32, true, WeightFormat<WF_E2M1>::PRIVATE_T}; return true;
-    case MXG_FP8_E4M3_BLOCK: f = {WF_BLOCK, 128, true, WeightFormat<WF_BLOCK>::PRIVATE_T}; return true;
+    case MXG_INT8: f = {WF_INT8, 16, true, WeightFormat<WF_INT8>::PRIVATE_T, WeightFormat<WF_INT8>::row_bytes}; return true;
+    case MXG_BF16: f = {WF_BF16, 8, false, WeightFormat<WF_BF16>::PRIVATE_T, WeightFormat<WF_BF16>::row_bytes}; return true;
+    case MXG_MXFP8_E4M3: f = {WF_E4M3, 32, true, WeightFormat<WF_E4M3>::PRIVATE_T, WeightFormat<WF_E4M3>::row_bytes}; return true;
+    case MXG_MXFP8_E5M2: f = {WF_E5M2, 32, true, WeightFormat<WF_E5M2>::PRIVATE_T, WeightFormat<WF_E5M2>::row_bytes}; return true;
+    case MXG_MXFP4_E2M1: f = {WF_E2M1, 32, true, WeightFormat<WF_E2M1>::PRIVATE_T, WeightFormat<WF_E2M1>::row_bytes}; return true;
+    case MXG_FP8_E4M3_BLOCK: f = {WF_BLOCK, 128, true, WeightFormat<WF_BLOCK>::PRIVATE_T, WeightFormat<WF_BLOCK>::row_bytes}; return true;
     default: return false;
   }
 }
@@ -141,9 +143,14 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   a.split_k = few && live * cdiv(a.N1, 64) < 2 * cu_count();
   a.up_tiles = (int)cdiv(a.N1, a.split_k ? 16 : 64);
   a.down_tiles = (int)cdiv(D, few ? 16 : 64);
-  // Few columns leave compute units idle: the records are split over several
-  // workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds their sums).
-  a.splits = few ? 1 : (int)std::max<int64_t>(1, EXP_SPLIT_BLOCKS / a.down_tiles);
+  // Few columns leave compute units idle: the list of the records' units is
+  // split over several workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds
+  // their sums).  A split costs its share of the last workgroup's additions, about
+  // 0.2 + 0.006 T us, and saves units: 0.8 us each, shared, and a quarter private.
+  const double units = (double)live * (double)cdiv(f.row_bytes(F), 128) / (few ? EXP_WAVES : 1);
+  const double best = std::sqrt(units * 0.8 / (0.2 + 0.006 * (double)T));
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(EXP_SPLIT_BLOCKS / a.down_tiles, (int64_t)best));
+  if (few && units < 24.0) a.splits = 1;
   // Up to 5 tokens per expert that has any: records of 8, whose smaller
   // stages leave room for more of them in flight; else 16 (an expert of more
   // tokens than that is read again).

@@ -8,17 +8,18 @@ namespace mxg {
 namespace {
 
 // Parts of the rows, from sizes alone (the workspace's size must not depend on
-// the device): about 2048 workgroups of at least 16 rows each; one part of
-// sixteen waves up to 256 rows (129 x 5002, GELU: 7.2 us, 9.9 in parts of 16).
+// the device): about 2048 workgroups of at least 32 rows each; one part of
+// sixteen waves up to 256 rows, 512 where the columns occupy the device (129 x 5002,
+// GELU: 7.2 us, 9.9 in parts of 16).
 struct GradShape {
   bool few;
   int64_t stripes, parts, rows;
 };
 GradShape grad_shape(int64_t M, int64_t N) {
   GradShape s;
-  s.few = M <= 256;
+  s.few = M <= 256 || (M <= 512 && N >= 8192);
   s.stripes = cdiv(N, s.few ? 64 * RG_FEW_V : 512);
-  s.rows = s.few ? M : std::max<int64_t>(16, cdiv(M, std::max<int64_t>(1, 2048 / s.stripes)));
+  s.rows = s.few ? M : std::max<int64_t>(32, cdiv(M, std::max<int64_t>(1, 2048 / s.stripes)));
   s.parts = cdiv(M, s.rows);
   return s;
 }
@@ -75,9 +76,9 @@ extern "C" int mxgemm_residual_backward(int activation, const void *dD, const vo
                                         int64_t N, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
   const int v = mxgemm_residual_backward_validate(activation, dD, z, dz, dbias, M, N, workspace, workspace_bytes);
   if (v != MXG_OK || N == 0) return v;
-  const unsigned sums = (unsigned)cdiv(N, 256);
+  const unsigned sums = (unsigned)cdiv(N, 64);
   if (M == 0) {
-    if (dbias) hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(256), 0, stream, nullptr, dbias, N, 0);
+    if (dbias) hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(64 * CS_WAVES), 0, stream, nullptr, dbias, N, 0);
     return launch_status();
   }
   const GradShape s = grad_shape(M, N);
@@ -93,6 +94,6 @@ extern "C" int mxgemm_residual_backward(int activation, const void *dD, const vo
   hipLaunchKernelGGL((s.few ? pick_grad<RG_FEW_V, 16>(activation) : pick_grad<8, 4>(activation)),
                      dim3((unsigned)s.stripes, (unsigned)s.parts), dim3(s.few ? 1024 : 256), 0, stream, a);
   if (dbias && s.parts > 1)
-    hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(256), 0, stream, (const float *)workspace, dbias, N, (int)s.parts);
+    hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(64 * CS_WAVES), 0, stream, (const float *)workspace, dbias, N, (int)s.parts);
   return launch_status();
 }

@@ -145,12 +145,32 @@ __global__ __launch_bounds__(64 * W) void residual_grad_kernel(ResidualGradArgs 
   }
 }
 
-// out[n] = sum of the parts, in order; none: 0.
-__global__ __launch_bounds__(256) void column_sums_kernel(const float *part, float *out, int64_t N, int parts) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+// out[n] = sum of the parts; none: 0.  64 columns per workgroup, part k to wave
+// k % 16, eight parts' loads in flight together, the waves' sums in their order
+// (one thread per column through all parts: 9327 x 146 took 140 us, 13 so).
+constexpr int CS_WAVES = 16;
+__global__ __launch_bounds__(64 * CS_WAVES) void column_sums_kernel(const float *part, float *out, int64_t N, int parts) {
+  __shared__ float sums[CS_WAVES][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
-  for (int k = 0; k < parts; ++k) s += part[(int64_t)k * N + n];
+  if (n < N) {
+    for (int k0 = w; k0 < parts; k0 += 8 * CS_WAVES) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j * CS_WAVES;
+        v[j] = k < parts ? part[(int64_t)k * N + n] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+    }
+  }
+  sums[w][lane] = s;
+  __syncthreads();
+  if (w != 0 || n >= N) return;
+#pragma unroll
+  for (int k = 1; k < CS_WAVES; ++k) s += sums[k][lane];
   out[n] = s;
 }
 

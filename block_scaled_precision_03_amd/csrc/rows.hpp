@@ -38,19 +38,18 @@ __device__ inline void rows_finish(const DenseArgs &p, v4f (*part)[FM * FN][64],
     const int64_t r = m0 + in, col = n0 + 16 * (f % FN) + 4 * q;
     if (in >= rows || r >= p.M || col >= p.N) continue;
     const int64_t o = r * p.N + col, room = p.N - col;
-    const bool wide = (p.N & 3) == 0;
     v4f near = {0.f, 0.f, 0.f, 0.f}, bias = {0.f, 0.f, 0.f, 0.f};
-    if (p.R) near = load_bf16x4(p.R + o, room, wide);
-    if (p.bias) bias = load_bf16x4(p.bias + col, room, false);
+    if (p.R) near = load_bf16x4(p.R + o, room);
+    if (p.bias) bias = load_bf16x4(p.bias + col, room);
     v4f v = part[0][f][lane];
 #pragma unroll
     for (int k = 1; k < W; ++k) v += part[k][f][lane];
     if constexpr (SMODE == SM_TENSOR) v = v * alpha;
     v += bias;
-    if (p.Z) store_bf16x4(p.Z + o, v, room, wide);
+    if (p.Z) store_bf16x4(p.Z + o, v, room);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = activate_select(p.act, v[k]);
-    store_bf16x4(p.D + o, v + near, room, wide);
+    store_bf16x4(p.D + o, v + near, room);
   }
 }
 

@@ -26,29 +26,29 @@ namespace mxg {
 
 constexpr int SBM = 64, SBN = 64;
 
-// Four consecutive values of a BF16 row of which `room` are left (8-byte
-// accesses where the row pitch allows, `wide`).
-__device__ inline void store_bf16x4(uint16_t *dst, const v4f &v, int64_t room, bool wide) {
+// Four consecutive values of a BF16 row of which `room` are left, in one access
+// at whatever alignment the row pitch leaves (the hardware takes any).
+__device__ inline void store_bf16x4(uint16_t *dst, const v4f &v, int64_t room) {
   const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-  if (room >= 4 && wide) {
-    *(v2i *)dst = (v2i){(int)u[0], (int)u[1]};
+  if (room >= 4) {
+    __builtin_memcpy(dst, u, 8);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 3; ++k)
       if (k < room) dst[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
   }
 }
-__device__ inline v4f load_bf16x4(const uint16_t *src, int64_t room, bool wide) {
-  if (room >= 4 && wide) {
-    const v2i u = *(const v2i *)src;
-    return (v4f){__uint_as_float((uint32_t)u.x << 16), __uint_as_float((uint32_t)u.x & 0xFFFF0000u),
-                 __uint_as_float((uint32_t)u.y << 16), __uint_as_float((uint32_t)u.y & 0xFFFF0000u)};
-  }
-  v4f v = {0.f, 0.f, 0.f, 0.f};
+__device__ inline v4f load_bf16x4(const uint16_t *src, int64_t room) {
+  uint32_t u[2] = {0, 0};
+  if (room >= 4) {
+    __builtin_memcpy(u, src, 8);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < room) v[k] = __uint_as_float((uint32_t)src[k] << 16);
-  return v;
+    for (int k = 0; k < 3; ++k)
+      if (k < room) u[k >> 1] |= (uint32_t)src[k] << (16 * (k & 1));
+  }
+  return (v4f){__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xFFFF0000u), __uint_as_float(u[1] << 16),
+               __uint_as_float(u[1] & 0xFFFF0000u)};
 }
 
 template <int FA, int FB, int SMODE, bool PSB, int FUSE>
@@ -193,17 +193,17 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs p) {
         }
         v += (v4f){bias[0], bias[1], bias[2], bias[3]};
         if constexpr (FUSE == FUSE_RES) {
-          if (p.Z) store_bf16x4(p.Z + r * p.N + col, v, p.N - col, (p.N & 3) == 0);
+          if (p.Z) store_bf16x4(p.Z + r * p.N + col, v, p.N - col);
         }
         v.x = activate(p.act, v.x);
         v.y = activate(p.act, v.y);
         v.z = activate(p.act, v.z);
         v.w = activate(p.act, v.w);
         if constexpr (FUSE == FUSE_RES) {
-          if (p.R) v += load_bf16x4(p.R + r * p.N + col, p.N - col, (p.N & 3) == 0);
+          if (p.R) v += load_bf16x4(p.R + r * p.N + col, p.N - col);
         }
       }
-      store_bf16x4(p.D + r * p.N + col, v, p.N - col, (p.N & 3) == 0);
+      store_bf16x4(p.D + r * p.N + col, v, p.N - col);
     }
   }
 }

@@ -733,9 +733,10 @@ int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float
  *         buffer as D (a layer's residual stream updated in place).
  * z       BF16 out [M, N], the activation's argument (with MXG_ACT_SWIGLU too
  *         [M, N]), 16-byte aligned, or NULL; no other argument's buffer.
- * With neither it is mxgemm_run_fused.  K = 0: z = bias.  Sums may be formed
- * in another order than mxgemm_run's (few rows split K over waves), so the two
- * can differ in the last bit.
+ * K = 0: z = bias.  Few rows or columns are computed by kernels of their own that
+ * split K over waves, with or without a residual, so that the FP32 sums' order,
+ * and with it the last bit, can differ from mxgemm_run_fused's (MXG_INT8 sums
+ * are exact: no difference).
  * Errors as mxgemm_run_fused; N above 4194304 is MXG_ERR_UNSUPPORTED, z the
  * same pointer as D or residual MXG_ERR_INVALID_ARG.
  *
@@ -764,7 +765,7 @@ int mxgemm_validate_residual(int fmtA, int fmtB, int layout, const void *A, cons
                              const void *sB, const void *D, int64_t M, int64_t N, int64_t K, const void *bias,
                              int activation, const void *residual, const void *z);
 /* MXG_DENSE_*: the kernel mxgemm_run_residual launches for these sizes on the
- * current device where it has a residual or z. */
+ * current device. */
 int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K);
 int64_t mxgemm_residual_backward_workspace_bytes(int64_t M, int64_t N);
 int mxgemm_residual_backward(int activation, const void *dD, const void *z, void *dz, float *dbias, int64_t M,

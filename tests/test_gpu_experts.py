@@ -179,6 +179,20 @@ def test_same_bits_every_time():
         assert torch.equal(c.run(), want)
 
 
+@pytest.mark.parametrize("name", sorted(R.FORMATS))
+@pytest.mark.parametrize("T", [1, 2, 5, 40])
+def test_few_columns_many_units(name, T):
+    """Lists split over workgroups, whose sums meet."""
+    u = R.UNIT[R.FORMATS[name]]
+    c = Case(R.FORMATS[name], T, 6, 4, max(u, 128), u * (2600 // u), seed=T)
+    c.check()
+    want = c.out.clone()
+    for _ in range(5):
+        c.ws.fill_(0xEE)
+        c.run()
+        assert torch.equal(c.out, want)
+
+
 def test_empty_sizes():
     c = Case(R.INT8, 3, 2, 1, 32, 16)
     m, d = _mx(), c.d

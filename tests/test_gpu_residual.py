@@ -201,13 +201,24 @@ def test_in_place(name, M, N, K):
     assert torch.equal(r, want)
 
 
-@pytest.mark.parametrize("name", ["mx44", "fp4", "tw44", "int8"])
-def test_without_residual_and_z_it_is_run_fused(name):
+@pytest.mark.parametrize("name", sorted(FORMATS))
+@pytest.mark.parametrize("M,N,K", [(1, 514, 2048), (130, 258, 512), (2148, 2306, 512)])
+def test_without_residual_and_z(name, M, N, K):
+    """Bias and activation alone, and nothing: integer sums as run_fused, bit for bit."""
     m = _mx()
-    c = Case(name, 130, 258, 512, a=R.ACT_GELU, residual=False, z=False)
-    D = torch.empty(130, 258, dtype=b16, device=DEV)
-    m.run_fused(c.fa, c.fb, m.NT, c.A, c.sA, c.B, c.sB, D, 130, 258, 512, bias=c.bias, activation=R.ACT_GELU)
-    assert torch.equal(c.run(), D)
+    for bias, a in ((True, R.ACT_GELU), (False, R.ACT_NONE)):
+        c = Case(name, M, N, K, a=a, bias=bias, residual=False, z=False)
+        c.check()
+        if name == "int8":
+            D = torch.empty(M, N, dtype=b16, device=DEV)
+            m.run_fused(c.fa, c.fb, m.NT, c.A, c.sA, c.B, c.sB, D, M, N, K, bias=c.bias, activation=a)
+            assert torch.equal(c.run(), D)
+
+
+@pytest.mark.parametrize("name", ["mx44", "mx54", "fp4", "tw54"])
+@pytest.mark.parametrize("N", [2305, 2306, 2308, 2310])
+def test_large_tiles_at_any_pitch(name, N):
+    Case(name, 2148, N, 512, a=R.ACT_RELU if N == 2306 else R.ACT_NONE, bias=N % 2 == 0, seed=N).check()
 
 
 @pytest.mark.parametrize("name", ["mx44", "int8"])
@@ -285,7 +296,7 @@ ALL = ACTS + [R.ACT_SWIGLU]
 
 
 @pytest.mark.parametrize("a", ALL)
-@pytest.mark.parametrize("M,N", [(1, 2), (1, 1000), (2, 8), (15, 514), (16, 512), (17, 510), (129, 5002), (256, 258), (257, 260), (300, 4608), (2000, 66)])
+@pytest.mark.parametrize("M,N", [(1, 2), (1, 1000), (2, 8), (15, 514), (16, 512), (17, 510), (129, 5002), (256, 258), (257, 260), (300, 4608), (2000, 66), (9327, 146)])
 def test_gradient(a, M, N):
     backward(a, M, N, seed=M, special=M * N > 100)
 
