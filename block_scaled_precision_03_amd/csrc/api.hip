@@ -95,6 +95,20 @@ extern "C" const char *mxgemm_status_string(int s) {
   }
 }
 
+namespace {
+// A kernel of each file that mxgemm_run_residual alone may launch from.
+int residual_kernels_init() {
+  const dense_fn fns[] = {pick_residual_mx_a4(F_E4M3, false, FUSE_RES), pick_residual_mx_a5(F_E4M3, false, FUSE_RES),
+                          pick_residual_tw_a4(F_E4M3, false, FUSE_RES), pick_residual_tw_a5(F_E4M3, false, FUSE_RES),
+                          pick_residual_fp4(false, FUSE_RES), pick_rows(F_E4M3, F_E4M3, true, false, 0),
+                          pick_small(F_E4M3, F_E4M3, true, false, FUSE_RES)};
+  hipFuncAttributes attr;
+  for (const dense_fn fn : fns)
+    if (hipFuncGetAttributes(&attr, (const void *)fn) != hipSuccess) return MXG_ERR_HIP;
+  return MXG_OK;
+}
+}  // namespace
+
 extern "C" int mxgemm_init(void) {
   // Touch the device so the code object is loaded before any graph capture.
   int dev = 0;
@@ -106,7 +120,8 @@ extern "C" int mxgemm_init(void) {
   int v = int8_init();
   if (v == MXG_OK) v = moe_init();
   if (v == MXG_OK) v = experts_init();
-  return v == MXG_OK ? residual_init() : v;
+  if (v == MXG_OK) v = residual_init();
+  return v == MXG_OK ? residual_kernels_init() : v;
 }
 
 extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, const void *sA,

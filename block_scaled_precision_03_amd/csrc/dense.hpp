@@ -581,8 +581,8 @@ struct DenseLoop {
     // Full tiles store through the range-checked vector offset (at most
     // 2 (255 N + 255) bytes from the tile's origin), which must stay below
     // the resource's clamped size of 2^31 - 16 bytes; wider D takes the
-    // element-wise path.  RES: at any alignment (the hardware takes any; row by
-    // row and element by element an odd pitch cost XX).
+    // element-wise path.  RES: at any alignment (the hardware takes any; 3273 x
+    // 11990 x 1792 MXFP4 102 us, 181 element by element).
     e.full = m0 + DBM <= lim && n0 + DBN <= p.N && (RES || (p.N & 7) == 0) && p.N <= (1 << 22);
     const int64_t org = m0 * p.N + n0;
     e.rd = rsrc4(p.D + org, clamp_records(2 * (p.M * p.N - org)));

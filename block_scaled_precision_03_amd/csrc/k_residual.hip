@@ -9,15 +9,15 @@ namespace {
 
 // Parts of the rows, from sizes alone (the workspace's size must not depend on
 // the device): about 2048 workgroups of at least 32 rows each; one part of
-// sixteen waves up to 256 rows, 512 where the columns occupy the device (129 x 5002,
-// GELU: 7.2 us, 9.9 in parts of 16).
+// sixteen waves up to 256 rows (129 x 5002, GELU: 7.2 us, 9.9 in parts of 16; 379 x 8966,
+// SwiGLU: 16.0 and 16.8).
 struct GradShape {
   bool few;
   int64_t stripes, parts, rows;
 };
 GradShape grad_shape(int64_t M, int64_t N) {
   GradShape s;
-  s.few = M <= 256 || (M <= 512 && N >= 8192);
+  s.few = M <= 256;
   s.stripes = cdiv(N, s.few ? 64 * RG_FEW_V : 512);
   s.rows = s.few ? M : std::max<int64_t>(32, cdiv(M, std::max<int64_t>(1, 2048 / s.stripes)));
   s.parts = cdiv(M, s.rows);
