@@ -4,6 +4,10 @@ gradients of its router and combine, on this library's entry points:
     route -> quantize into the experts' rows -> gate and up product with
     SwiGLU -> quantize -> down product -> combine
 
+and, for a few tokens (a decode step), in three launches from the same weights:
+
+    route -> the chosen experts on unquantized activations, with the residual
+
 Everything but the weights' layout runs on the device from buffers that the
 layer keeps, without a host read, so a step can be captured into a graph.
 
@@ -43,6 +47,8 @@ class Int8MoE:
         self.y, self.out = new(b16, n, D), new(b16, T, D)
         self.dy, self.dweights, self.dlogits = new(b16, n, D), new(f32, T, topk), new(f32, T, E)
         self.workspace = new(torch.uint8, max(1, mx.moe_route_workspace_bytes(T, E)))
+        self.max_few = min(T, 64)
+        self.few_workspace = new(torch.uint8, mx.moe_experts_workspace_bytes(self.max_few, topk, F))
         self.max_tokens = T
 
     @staticmethod
@@ -77,6 +83,21 @@ class Int8MoE:
         mx.quantize_int8(mx.BF16, self.h, self.hq, self.hs, n, F)
         mx.grouped_int8_run(E, self.sizes, self.hq, self.hs, self.w2, self.s2, self.y, n, D, F)
         mx.moe_combine(self.y, self.weights, self.row_of, self.out, T, k, D, n)
+        return self.out[:T]
+
+    def decode(self, x, logits, residual=None):
+        """forward for at most 64 tokens, plus `residual` (BF16, x's shape).
+        The activations stay in BF16 and FP32, so its result is closer to the
+        FP32 layer's than forward's."""
+        self._check(x, logits)
+        T, k = x.shape[0], self.k
+        if T > self.max_few:
+            raise ValueError("%d tokens, decode takes %d" % (T, self.max_few))
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or not residual.is_contiguous()):
+            raise ValueError("expected a residual like x")
+        mx.moe_route(mx.F32, logits, None, self.ids, self.weights, T, self.E, k)
+        mx.moe_experts(mx.INT8, x, self.ids, self.weights, self.w1, self.s1, self.w2, self.s2, self.out, T, self.E, k, self.D,
+                       self.F, residual=residual, workspace=self.few_workspace)
         return self.out[:T]
 
     def backward(self, dout, logits):

@@ -97,3 +97,25 @@ def test_reference_is_the_formula(name):
                     h = [z[2 * f] / (1 + np.exp(-z[2 * f])) * z[2 * f + 1] for f in range(F)]
                     s += float(w[t, j]) * sum(float(v2[ids[t, j], d, f]) * h[f] for f in range(F))
             assert abs(out[t, d] - s) <= 1e-9 * max(1.0, abs(s)) and tol[t, d] > 0
+
+
+def test_example_decode_refuses(monkeypatch):
+    """What does not fit the example layer's decode step reaches no library call."""
+    import torch
+    from examples import int8_moe_layer as ex
+    z = lambda dt, *s: torch.zeros(*s, dtype=dt)
+    monkeypatch.setattr(ex.Int8MoE, "_quantize", staticmethod(lambda w: (z(torch.int8, *w.shape), z(torch.float32, *w.shape[:2]))))
+
+    def called(*args, **kw):
+        raise AssertionError("a library call was made")
+    w = torch.zeros(8, 48, 32)
+    layer = ex.Int8MoE(w, w, torch.zeros(8, 32, 48), 2, 100)
+    for name in ("moe_route", "moe_experts"):
+        monkeypatch.setattr(ex.mx, name, called)
+    x, l = z(torch.bfloat16, 4, 32), z(torch.float32, 4, 8)
+    for a, b, r in ((z(torch.bfloat16, 65, 32), z(torch.float32, 65, 8), None), (x.float(), l, None), (x, l[:3], None), (x, l, x[:3]),
+                    (x, l, x.float()), (x, l, z(torch.bfloat16, 32, 4).t())):
+        with pytest.raises(ValueError):
+            layer.decode(a, b, residual=r)
+    with pytest.raises(AssertionError, match="library call"):
+        layer.decode(z(torch.bfloat16, 64, 32), z(torch.float32, 64, 8), residual=z(torch.bfloat16, 64, 32))
