@@ -108,6 +108,27 @@ def test_an_expert_named_twice_counts_with_both_weights():
     Case(R.INT8, 40, 2, 32, 64, 64, ids=np.random.default_rng(1).integers(-1, 3, (40, 32))).check()
 
 
+@pytest.mark.parametrize("T", [1, 2])
+def test_most_slots_of_one_and_two_tokens(T):
+    """The choice of one or two tokens is read in registers: up to 64 slots,
+    named in any order, twice, by both tokens, or not at all."""
+    rng = np.random.default_rng(T)
+    for ids in (rng.integers(-1, 4, (T, 32)), rng.permutation(200)[:32 * T].reshape(T, 32), np.full((T, 32), -1),
+                np.concatenate([np.full((T, 31), 1 << 20), np.full((T, 1), 3)], 1), np.full((T, 32), 199)):
+        Case(R.INT8, T, 200, 32, 48, 32, ids=ids, seed=T).check()
+    if T == 2:
+        # the second token alone, and the first alone, name an expert
+        Case(R.E4M3, 2, 5, 2, 64, 64, ids=[[3, -1], [4, 3]]).check()
+        Case(R.E4M3, 2, 5, 2, 64, 64, ids=[[-1, -1], [4, 0]]).check()
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("D,F", [(131072, 16), (16, 131072)])
+def test_longest_rows(T, D, F):
+    c = Case(R.INT8, T, 2, 1, D, F, ids=np.arange(T)[:, None] % 2, a=R.ACT_NONE)
+    c.check()
+
+
 def test_most_experts():
     Case(R.INT8, 64, 1024, 32, 16, 16, seed=2).check()
     Case(R.INT8, 1, 1024, 32, 16, 16, seed=3).check()
