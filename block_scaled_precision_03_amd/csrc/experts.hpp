@@ -382,8 +382,6 @@ struct SlotTable {
   int head;                                    // first lane with this expert
   uint32_t tokens;                             // tokens that name it
   int base;                                    // its first pair
-  float share;                                 // of the lane's token
-  bool lead;                                   // first slot of its token with this expert
   uint64_t heads;                              // lanes that are their expert's first
 };
 
@@ -393,28 +391,16 @@ __device__ inline SlotTable slot_table(const ExpertsArgs &p) {
   SlotTable s;
   s.e = -1;
   s.t = lane / p.topk;
-  float w = 0.0f;
-  if (lane < P) {
-    s.e = p.ids[lane];
-    w = p.w[lane];
-    if (s.e < 0 || s.e >= p.E) s.e = -1;
-  }
+  if (lane < P) s.e = p.ids[lane];
+  if (s.e < 0 || s.e >= p.E) s.e = -1;
   s.head = lane;
   s.tokens = 0;
-  s.share = 0.0f;
-  s.lead = s.e >= 0;
   for (int k = P - 1; k >= 0; --k) {
     const int e = __builtin_amdgcn_readlane(s.e, k), t = k >= p.topk;
     if (s.e >= 0 && e == s.e) {
       s.head = k < s.head ? k : s.head;
       s.tokens |= 1u << t;
-      if (t == s.t && k < lane) s.lead = false;
     }
-  }
-  for (int k = 0; k < P; ++k) {
-    const int e = __builtin_amdgcn_readlane(s.e, k), t = k >= p.topk;
-    const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
-    if (s.e >= 0 && e == s.e && t == s.t) s.share += wk;
   }
   s.heads = __ballot(s.e >= 0 && s.head == lane);
   const uint64_t both = __ballot(s.tokens == 3u) & s.heads;
@@ -435,13 +421,23 @@ __device__ inline ExpertRec find_record(const SlotTable &s, int rank, uint64_t &
 
 __device__ inline void expert_table(const ExpertsArgs &p, const SlotTable &s) {
   const int lane = threadIdx.x & 63;
-  const int base = __shfl(s.base, s.head);
+  const int base = __shfl(s.base, s.head), P = p.T * p.topk;
   for (int i = threadIdx.x; i < p.down_tiles; i += blockDim.x)
     if (p.splits > 1) p.arrived[i] = 0;
   if (threadIdx.x >= 64) return;
+  const float w = lane < P ? p.w[lane] : 0.0f;
+  float share = 0.0f;                          // of the lane's token
+  bool lead = s.e >= 0;                        // first slot of its token with this expert
+  for (int k = 0; k < P; ++k) {
+    const int e = __builtin_amdgcn_readlane(s.e, k), t = k >= p.topk;
+    const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
+    if (s.e < 0 || e != s.e || t != s.t) continue;
+    share += wk;
+    lead &= k >= lane;
+  }
   if (lane == 0) *p.count = __popcll(s.heads);
   if (s.heads >> lane & 1) p.rec[__popcll(s.heads & ((1ull << lane) - 1))] = ExpertRec{s.e, s.base, (int32_t)__popc(s.tokens), 0};
-  if (s.lead) p.pair[base + (s.t == 1 && (s.tokens & 1u) ? 1 : 0)] = ExpertPair{s.t, s.share};
+  if (lead) p.pair[base + (s.t == 1 && (s.tokens & 1u) ? 1 : 0)] = ExpertPair{s.t, share};
 }
 
 // h of four consecutive rows of W1 (two SwiGLU pairs), as two BF16 each.

@@ -129,6 +129,17 @@ def test_longest_rows(T, D, F):
     c.check()
 
 
+@pytest.mark.parametrize("name", sorted(R.FORMATS))
+@pytest.mark.parametrize("T", [1, 2])
+def test_many_rows_of_the_first_weight(name, T):
+    """One or two tokens, enough short rows for 64 of them per workgroup (the
+    last of them not full), and so many that K is long as well."""
+    u = R.UNIT[R.FORMATS[name]]
+    F = u * (3300 // u) + (u if u < 64 else 0)
+    Case(R.FORMATS[name], T, 4, 4, u * (280 // u), F, seed=T).check()
+    Case(R.FORMATS[name], T, 4, 1, u * (6200 // u), u * max(300 // u, 1), a=R.ACT_NONE, seed=T).check()
+
+
 def test_most_experts():
     Case(R.INT8, 64, 1024, 32, 16, 16, seed=2).check()
     Case(R.INT8, 1, 1024, 32, 16, 16, seed=3).check()
