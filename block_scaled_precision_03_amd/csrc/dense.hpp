@@ -556,7 +556,8 @@ struct DenseLoop {
   // that every lane holds 8 consecutive columns: lanes with q even get
   // columns 8(q/2) .. +7 of tile 2p, lanes with q odd those of tile 2p+1.  One
   // 16-byte store per lane then covers 64 contiguous bytes of 16 rows.  Edge
-  // tiles (and N not a multiple of 8) store element by element with masks.
+  // tiles (and N not a multiple of 8) store element by element with masks (with
+  // a residual like full ones, see store_rows).
   struct Epi {
     u32x4 rd;                    // full tiles: D from the tile's origin
     uint32_t voff;               // full tiles: this lane's byte offset in the tile
@@ -581,9 +582,9 @@ struct DenseLoop {
     // Full tiles store through the range-checked vector offset (at most
     // 2 (255 N + 255) bytes from the tile's origin), which must stay below
     // the resource's clamped size of 2^31 - 16 bytes; wider D takes the
-    // element-wise path.  RES: at any alignment (the hardware takes any; 3273 x
-    // 11990 x 1792 MXFP4 102 us, 181 element by element).
-    e.full = m0 + DBM <= lim && n0 + DBN <= p.N && (RES || (p.N & 7) == 0) && p.N <= (1 << 22);
+    // element-wise path.  RES: N is at most 2^22, and edge tiles store like full
+    // ones (see store_rows); full: no column past N.
+    e.full = RES ? n0 + DBN <= p.N : m0 + DBM <= lim && n0 + DBN <= p.N && (p.N & 7) == 0 && p.N <= (1 << 22);
     const int64_t org = m0 * p.N + n0;
     e.rd = rsrc4(p.D + org, clamp_records(2 * (p.M * p.N - org)));
     e.rowstride = (uint32_t)(32 * p.N);
@@ -591,10 +592,12 @@ struct DenseLoop {
     e.voff = (uint32_t)(2 * ((c.wm * (FM * 16) + i) * p.N + c.wn * (FN * 16) + 16 * (q & 1) + 8 * (q >> 1)));
   }
 
-  // The residual beside row tile a of a full tile: lane (i, q) holds row 16 a
+  // The residual beside row tile a: lane (i, q) holds row 16 a
   // + i, columns 16 b + 4 q .. + 3 of the wave's block, as its sums do.  The
   // offsets are those of the stores (see make_epi), so the same sizes bound
   // them.  Without a residual the resource is empty: zeros, no memory read.
+  // What a lane loads past its row's end, of the next row, is not used; past
+  // the last row it gets zeros.
   typedef v2i ResRow[RES ? FN : 1];
   __device__ static inline void load_residual(const Ctx &c, const Epi &e, int a, ResRow &r) {
     if constexpr (RES) {
@@ -609,6 +612,18 @@ struct DenseLoop {
 #pragma unroll
       for (int b = 0; b < FN; ++b)
         r[b] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rr, (int)(o + 32u * b), 0, 0));
+      if ((p.N & 1) && !e.full && e.m0 + DBM >= p.M) {
+        // the matrix's last element may be half a dword at the resource's end,
+        // which the load above drops whole
+#pragma unroll
+        for (int b = 0; b < FN; ++b) {
+          const int last = (int)(p.N - 1) - e.n0 - (c.wn * (FN * 16) + b * 16 + 4 * q);
+          const bool here = last == 0 || last == 2;
+          const uint32_t h = __builtin_amdgcn_raw_buffer_load_b16(rr, (int)(here ? o + 32u * b + 2u * last : 0x80000000u), 0, 0);
+          if (last == 0) r[b].x = (int)(((uint32_t)r[b].x & 0xFFFF0000u) | h);
+          if (last == 2) r[b].y = (int)(((uint32_t)r[b].y & 0xFFFF0000u) | h);
+        }
+      }
     }
   }
 
@@ -657,14 +672,21 @@ struct DenseLoop {
       }
       return v;
     };
-    if (e.full) {
+    if (RES || e.full) {
       // computed here, not hoisted into a register per row tile
       uint32_t rs = e.rowstride;
       asm volatile("" : "+s"(rs));
       const int lane = (int)__lane_id();
       const bool odd = ((lane >> 4) & 1) != 0;
       const int partner = (lane ^ 16) << 2;
-      auto put = [&](const v4f &x, const v4f &y, const u32x4 &rd, int pr) {
+      // RES: at any alignment (the hardware takes any), and the row's offset in
+      // the vector offset, which the range check sees: rows past M lie past the
+      // resource's end.  Where columns past N are in the tile, a lane whose eight
+      // columns do not all exist stores those that do one by one (2489 x 9776 x
+      // 2304 MXFP4 with a residual 51.5 us, 88 with edge tiles element by element;
+      // 2489 x 9773, GELU and z 96, 116).
+      const uint32_t vo = RES ? e.voff + (uint32_t)a * rs : e.voff;
+      auto put = [&](const v4f &x, const v4f &y, const u32x4 &rd, uint16_t *out, int pr) {
         const uint32_t xlo = pack_bf16x2(x.x, x.y), xhi = pack_bf16x2(x.z, x.w);
         const uint32_t ylo = pack_bf16x2(y.x, y.y), yhi = pack_bf16x2(y.z, y.w);
         // q even keeps its tile-2p chunk and takes the partner's; q odd the
@@ -673,7 +695,26 @@ struct DenseLoop {
         const uint32_t rhi = (uint32_t)__builtin_amdgcn_ds_bpermute(partner, (int)(odd ? xhi : yhi));
         const v4i v = odd ? (v4i){(int)rlo, (int)rhi, (int)ylo, (int)yhi}
                           : (v4i){(int)xlo, (int)xhi, (int)rlo, (int)rhi};
-        store16_asm(v, rd, e.voff, (uint32_t)a * rs + 64u * pr);
+        if constexpr (RES) {
+          if (e.full) {
+            store16_asm(v, rd, vo, 64u * pr);
+          } else {
+            const int64_t N = c.p->N;
+            const int q = lane >> 4, room = (int)(N - e.n0) - (c.wn * (FN * 16) + 32 * pr + 16 * (q & 1) + 8 * (q >> 1));
+            store16_asm(v, rd, room >= 8 ? vo : 0x80000000u, 64u * pr);
+            // one 32-column block has such lanes
+            if ((N & 7) && (int)(N - e.n0) >> 5 == 2 * c.wn + pr) {
+              const int64_t org = (int64_t)e.m0 * N + e.n0;
+              const __amdgpu_buffer_rsrc_t rb = make_rsrc(out + org, clamp_records(2 * (c.p->M * N - org)));
+#pragma unroll
+              for (int k = 0; k < 7; ++k)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[k >> 1] >> (16 * (k & 1))), rb,
+                                                      (int)(k < room && room < 8 ? vo + 64u * pr + 2u * k : 0x80000000u), 0, 0);
+            }
+          }
+        } else {
+          store16_asm(v, rd, vo, (uint32_t)a * rs + 64u * pr);
+        }
       };
 #pragma unroll
       for (int pr = 0; pr < FN / 2; ++pr) {
@@ -682,44 +723,11 @@ struct DenseLoop {
           const DenseArgs &p = *c.p;
           if (p.Z) {
             const int64_t org = (int64_t)e.m0 * p.N + e.n0;
-            put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))), pr);
+            put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))), p.Z, pr);
           }
-          put(activated(x, res[2 * pr]), activated(y, res[2 * pr + 1]), e.rd, pr);
+          put(activated(x, res[2 * pr]), activated(y, res[2 * pr + 1]), e.rd, p.D, pr);
         } else {
-          put(activated(x, v2i{}), activated(y, v2i{}), e.rd, pr);
-        }
-      }
-    } else if constexpr (RES) {
-      // edge tiles, element by element through range-checked offsets (N is at
-      // most 2^22): those of no row or column go past any resource
-      const DenseArgs &p = *c.p;
-      int lane = (int)__lane_id();
-      asm volatile("" : "+v"(lane));       // offsets formed here, not kept from row tile to row tile
-      const int i = lane & 15, q = lane >> 4;
-      const int64_t org = (int64_t)e.m0 * p.N + e.n0;
-      const uint32_t left = clamp_records(2 * (p.M * p.N - org));
-      const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + org, left);
-      const __amdgpu_buffer_rsrc_t rr = p.R ? make_rsrc(p.R + org, left) : make_rsrc(p.D, 0);
-      const __amdgpu_buffer_rsrc_t rz = p.Z ? make_rsrc(p.Z + org, left) : make_rsrc(p.D, 0);
-      const int r = c.wm * (FM * 16) + a * 16 + i;
-      const bool in = (int64_t)e.m0 + r < e.lim;
-#pragma unroll
-      for (int b = 0; b < FN; ++b) {
-        const int col = c.wn * (FN * 16) + b * 16 + 4 * q;
-        uint32_t o[4], near[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[k] = in && e.n0 + col + k < p.N ? (uint32_t)(2 * (r * p.N + col + k)) : 0x80000000u;
-          near[k] = __builtin_amdgcn_raw_buffer_load_b16(rr, (int)o[k], 0, 0);
-        }
-        const v4f z = finish(row[b], b);
-        const v4f v = activated(z, (v2i){(int)(near[0] | near[1] << 16), (int)(near[2] | near[3] << 16)});
-        const uint32_t uz[2] = {pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w)};
-        const uint32_t u[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(uz[k >> 1] >> (16 * (k & 1))), rz, (int)o[k], 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(u[k >> 1] >> (16 * (k & 1))), rd, (int)o[k], 0, 0);
+          put(activated(x, v2i{}), activated(y, v2i{}), e.rd, nullptr, pr);
         }
       }
     } else {
@@ -746,24 +754,22 @@ struct DenseLoop {
   // steps: its loads and the stores share one counter, in order, so that spread
   // over the next step each row tile's residual would wait for the stores
   // of the row tile before it, and to load it whole the step has no registers left
-  // (16384 x 4096 x 4096, MXFP8: 267 us; so 246, 212 with the bias alone).  The
+  // (16384 x 4096 x 4096, MXFP8: 267 us; so 245 to 251, 210 with the bias alone).  The
   // next tile's first stage is already on its way.
   __device__ static inline void finish_tile(const Ctx &c, const Epi &e, const v4f (&acc)[FM][FN]) {
     // As many row tiles' residuals at once as registers allow; a later one's
     // loads are behind the stores of row tiles finished long before its turn.
-    constexpr int WIN = FUSE != FUSE_RES_ACT ? FM : FP4 || (MX && !PSB) ? 3 : 4;
+    constexpr int WIN = FUSE != FUSE_RES_ACT ? FM : FP4 || (MX && !PSB) ? 3 : 5;
     ResRow res[WIN];
     if constexpr (RES) {
-      if (e.full) {
 #pragma unroll
-        for (int a = 0; a < WIN; ++a) load_residual(c, e, a, res[a]);
-      }
+      for (int a = 0; a < WIN; ++a) load_residual(c, e, a, res[a]);
     }
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
       store_rows(c, e, a, acc[a], res[a % WIN]);
       if constexpr (RES) {
-        if (e.full && a + WIN < FM) load_residual(c, e, a + WIN, res[a % WIN]);
+        if (a + WIN < FM) load_residual(c, e, a + WIN, res[a % WIN]);
       }
     }
   }

@@ -24,6 +24,14 @@
 //     of out), the list split over the waves, whose sums meet at the end.
 //   shared: 64 rows, 16 per wave, one ring; the activations of a stage, up to 16
 //     rows of them, are brought once for all four waves.
+// Both sides for one token, the kernels' us, private and shared: 4 of 1024 x 512 INT8
+// 5.0 + 5.5, 7.5 + 6.8; 8 of 7168 x 2304 MXFP4 33 + 21, 34 + 24.
+//
+// Bound by memory where the experts are large: 16 tokens, 8 each, 64 experts of
+// 7168 x 2304 INT8, SwiGLU 493 us, 5.7 TB/s of weights (records of up to 8 tokens; a fifth wave
+// that does the loads: 428 + 255 us in place of 319 + 200); 1 token, 8 of them
+// in MXFP4 53 us, 3.7 TB/s.  By the two kernels' starts where they are small (1 token, 4
+// of 1024 x 512: 9.3 us).
 #pragma once
 #include "small.hpp"
 

@@ -221,6 +221,22 @@ def test_large_tiles_at_any_pitch(name, N):
     Case(name, 2148, N, 512, a=R.ACT_RELU if N == 2306 else R.ACT_NONE, bias=N % 2 == 0, seed=N).check()
 
 
+@pytest.mark.parametrize("name", ["mx45", "fp4", "tw44"])
+@pytest.mark.parametrize("past", [3, 5, 7, 8, 29, 61, 129, 255])
+def test_last_columns_of_large_tiles(name, past):
+    """Last column tiles of any width, the last row tile one row high, the
+    residual replaced in place, z beside it."""
+    m = _mx()
+    M, N = 2305, 2048 + past
+    c = Case(name, M, N, 512, a=R.ACT_SILU if past & 8 else R.ACT_NONE, bias=False, seed=past)
+    assert m.residual_variant(c.fa, c.fb, m.NT, M, N, 512) == m.DENSE_TILE256
+    c.check()
+    want = c.rows(c.D).clone()
+    c.rows(c.D).copy_(c.r)
+    c.run(residual=c.rows(c.D))
+    assert torch.equal(c.rows(c.D), want)
+
+
 @pytest.mark.parametrize("name", ["mx44", "int8"])
 def test_no_k_and_no_rows(name):
     m = _mx()
