@@ -686,7 +686,7 @@ struct DenseLoop {
       // 2304 MXFP4 with a residual 51.5 us, 88 with edge tiles element by element;
       // 2489 x 9773, GELU and z 96, 116).
       const uint32_t vo = RES ? e.voff + (uint32_t)a * rs : e.voff;
-      auto put = [&](const v4f &x, const v4f &y, const u32x4 &rd, uint16_t *out, int pr) {
+      auto put = [&](auto edge, const v4f &x, const v4f &y, const u32x4 &rd, uint16_t *out, int pr) {
         const uint32_t xlo = pack_bf16x2(x.x, x.y), xhi = pack_bf16x2(x.z, x.w);
         const uint32_t ylo = pack_bf16x2(y.x, y.y), yhi = pack_bf16x2(y.z, y.w);
         // q even keeps its tile-2p chunk and takes the partner's; q odd the
@@ -696,7 +696,7 @@ struct DenseLoop {
         const v4i v = odd ? (v4i){(int)rlo, (int)rhi, (int)ylo, (int)yhi}
                           : (v4i){(int)xlo, (int)xhi, (int)rlo, (int)rhi};
         if constexpr (RES) {
-          if (e.full) {
+          if (!edge) {
             store16_asm(v, rd, vo, 64u * pr);
           } else {
             const int64_t N = c.p->N;
@@ -716,20 +716,28 @@ struct DenseLoop {
           store16_asm(v, rd, vo, (uint32_t)a * rs + 64u * pr);
         }
       };
+      auto all = [&](auto edge) {
 #pragma unroll
-      for (int pr = 0; pr < FN / 2; ++pr) {
-        const v4f x = finish(row[2 * pr], 2 * pr), y = finish(row[2 * pr + 1], 2 * pr + 1);
-        if constexpr (RES) {
-          const DenseArgs &p = *c.p;
-          if (p.Z) {
-            const int64_t org = (int64_t)e.m0 * p.N + e.n0;
-            put(x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))), p.Z, pr);
+        for (int pr = 0; pr < FN / 2; ++pr) {
+          const v4f x = finish(row[2 * pr], 2 * pr), y = finish(row[2 * pr + 1], 2 * pr + 1);
+          if constexpr (RES) {
+            const DenseArgs &p = *c.p;
+            if (p.Z) {
+              const int64_t org = (int64_t)e.m0 * p.N + e.n0;
+              put(edge, x, y, rsrc4(p.Z + org, clamp_records(2 * (p.M * p.N - org))), p.Z, pr);
+            }
+            put(edge, activated(x, res[2 * pr]), activated(y, res[2 * pr + 1]), e.rd, p.D, pr);
+          } else {
+            put(edge, activated(x, v2i{}), activated(y, v2i{}), e.rd, nullptr, pr);
           }
-          put(activated(x, res[2 * pr]), activated(y, res[2 * pr + 1]), e.rd, p.D, pr);
-        } else {
-          put(activated(x, v2i{}), activated(y, v2i{}), e.rd, nullptr, pr);
         }
-      }
+      };
+      // Without an activation a branch for the whole row tile (16384 x 4096 x 14336
+      // MXFP8 765 us, 775 with one at each store); with one the latter (2489 x 9776
+      // x 2304, GELU, 95 us, 100).
+      if constexpr (FUSE == FUSE_RES_ACT) all(!e.full);
+      else if (!RES || e.full) all(std::false_type{});
+      else if constexpr (RES) all(std::true_type{});
     } else {
       // edge tiles: lane position recomputed here rather than kept live
       const DenseArgs &p = *c.p;

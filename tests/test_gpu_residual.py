@@ -221,6 +221,16 @@ def test_large_tiles_at_any_pitch(name, N):
     Case(name, 2148, N, 512, a=R.ACT_RELU if N == 2306 else R.ACT_NONE, bias=N % 2 == 0, seed=N).check()
 
 
+@pytest.mark.parametrize("name", ["mx44", "fp4", "tw54"])
+@pytest.mark.parametrize("M,N,K", [(635, 194, 2304), (2049, 62, 768), (5000, 130, 512), (777, 770, 1280)])
+def test_few_tiles_of_many_rows(name, M, N, K):
+    m = _mx()
+    for psb in (False, True):
+        c = Case(name, M, N, K, a=R.ACT_GELU if psb else R.ACT_NONE, psb=psb, seed=M)
+        assert m.residual_variant(c.fa, c.fb, m.NT, M, N, K) == m.DENSE_ROWS
+        c.check()
+
+
 @pytest.mark.parametrize("name", ["mx45", "fp4", "tw44"])
 @pytest.mark.parametrize("past", [3, 5, 7, 8, 29, 61, 129, 255])
 def test_last_columns_of_large_tiles(name, past):
