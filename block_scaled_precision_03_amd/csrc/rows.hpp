@@ -1,4 +1,4 @@
-// Dense NT GEMM for few rows or columns, MX and tensor-wise formats, with the
+// Dense NT GEMM for few rows or columns (or few tiles), MX and tensor-wise formats, with the
 // residual epilogue (mxgemm_run_residual): AR rows x 16 FN columns per workgroup
 // of W waves that split K between them; their sums meet in LDS in a fixed order.
 // The 64 x 64 tiles of small.hpp leave most compute units idle there and walk

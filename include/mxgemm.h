@@ -733,8 +733,8 @@ int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float
  *         buffer as D (a layer's residual stream updated in place).
  * z       BF16 out [M, N], the activation's argument (with MXG_ACT_SWIGLU too
  *         [M, N]), 16-byte aligned, or NULL; no other argument's buffer.
- * K = 0: z = bias.  Few rows or columns are computed by kernels of their own that
- * split K over waves, with or without a residual, so that the FP32 sums' order,
+ * K = 0: z = bias.  Few rows or columns, and other results of few tiles, are
+ * computed by kernels of their own that split K over waves, with or without a residual, so that the FP32 sums' order,
  * and with it the last bit, can differ from mxgemm_run_fused's (MXG_INT8 sums
  * are exact: no difference).
  * Errors as mxgemm_run_fused; N above 4194304 is MXG_ERR_UNSUPPORTED, z the
