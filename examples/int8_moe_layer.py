@@ -47,7 +47,9 @@ class Int8MoE:
         self.y, self.out = new(b16, n, D), new(b16, T, D)
         self.dy, self.dweights, self.dlogits = new(b16, n, D), new(f32, T, topk), new(f32, T, E)
         self.workspace = new(torch.uint8, max(1, mx.moe_route_workspace_bytes(T, E)))
+        # a decode step's own choice: forward's waits for its backward
         self.max_few = min(T, 64)
+        self.few_ids, self.few_weights = new(i32, self.max_few, topk), new(f32, self.max_few, topk)
         self.few_workspace = new(torch.uint8, mx.moe_experts_workspace_bytes(self.max_few, topk, F))
         self.max_tokens = T
 
@@ -88,16 +90,17 @@ class Int8MoE:
     def decode(self, x, logits, residual=None):
         """forward for at most 64 tokens, plus `residual` (BF16, x's shape).
         The activations stay in BF16 and FP32, so its result is closer to the
-        FP32 layer's than forward's."""
+        FP32 layer's than forward's.  It returns a view of the buffer that
+        forward's result is in, and leaves what backward needs as it is."""
         self._check(x, logits)
         T, k = x.shape[0], self.k
         if T > self.max_few:
             raise ValueError("%d tokens, decode takes %d" % (T, self.max_few))
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or not residual.is_contiguous()):
             raise ValueError("expected a residual like x")
-        mx.moe_route(mx.F32, logits, None, self.ids, self.weights, T, self.E, k)
-        mx.moe_experts(mx.INT8, x, self.ids, self.weights, self.w1, self.s1, self.w2, self.s2, self.out, T, self.E, k, self.D,
-                       self.F, residual=residual, workspace=self.few_workspace)
+        mx.moe_route(mx.F32, logits, None, self.few_ids, self.few_weights, T, self.E, k)
+        mx.moe_experts(mx.INT8, x, self.few_ids, self.few_weights, self.w1, self.s1, self.w2, self.s2, self.out, T, self.E, k,
+                       self.D, self.F, residual=residual, workspace=self.few_workspace)
         return self.out[:T]
 
     def backward(self, dout, logits):

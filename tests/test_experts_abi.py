@@ -119,3 +119,37 @@ def test_example_decode_refuses(monkeypatch):
             layer.decode(a, b, residual=r)
     with pytest.raises(AssertionError, match="library call"):
         layer.decode(z(torch.bfloat16, 64, 32), z(torch.float32, 64, 8), residual=z(torch.bfloat16, 64, 32))
+
+
+def test_example_decode_leaves_a_pending_backward(monkeypatch):
+    """forward, decode, backward: the gradients see forward's choice and rows."""
+    import torch
+    from examples import int8_moe_layer as ex
+    z = lambda dt, *s: torch.zeros(*s, dtype=dt)
+    monkeypatch.setattr(ex.Int8MoE, "_quantize", staticmethod(lambda w: (z(torch.int8, *w.shape), z(torch.float32, *w.shape[:2]))))
+    calls, seen = [], []
+
+    def route(dtype, logits, bias, ids, weights, *args, row_of=None, **kw):
+        calls.append("route")
+        for t in (ids, weights, row_of):
+            if t is not None:
+                t.fill_(len(calls))
+
+    def combine(y, weights, row_of, out, *args):
+        y.fill_(7)
+
+    for name in ("quantize_int8", "grouped_int8_run", "moe_experts"):
+        monkeypatch.setattr(ex.mx, name, lambda *args, **kw: None)
+    monkeypatch.setattr(ex.mx, "moe_route", route)
+    monkeypatch.setattr(ex.mx, "moe_combine", combine)
+    monkeypatch.setattr(ex.mx, "moe_combine_backward", lambda dout, y, w, row_of, *args: seen.extend([(y, 7), (w, 1), (row_of, 1)]))
+    monkeypatch.setattr(ex.mx, "moe_route_backward", lambda dtype, logits, ids, *args: seen.append((ids, 1)))
+    w = torch.zeros(8, 48, 32)
+    layer = ex.Int8MoE(w, w, torch.zeros(8, 32, 48), 2, 100)
+    x, l = z(torch.bfloat16, 4, 32), z(torch.float32, 4, 8)
+    layer.forward(x, l)
+    layer.decode(x[:3], l[:3])
+    layer.backward(x, l)
+    assert calls == ["route", "route"] and len(seen) == 4
+    for t, want in seen:
+        assert (t == want).all()

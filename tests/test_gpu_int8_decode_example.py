@@ -42,3 +42,24 @@ def test_decode():
         layer.decode(x, logits)
     with pytest.raises(ValueError):
         layer.decode(x[:3], logits[:3], residual=x[:2])
+
+
+def test_decode_between_forward_and_backward():
+    """Gradients of a step with a decode of other tokens inside are the step's own."""
+    from examples import int8_moe_layer as ex
+    from block_scaled_precision_03_amd import mxgemm as m
+    m.init()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    rand = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    E, F, D, k, T = 8, 96, 160, 2, 40
+    layer = ex.Int8MoE(rand(E, F, D) * D ** -0.5, rand(E, F, D) * D ** -0.5, rand(E, D, F) * F ** -0.5, k, T)
+    x, logits, dout = rand(T, D).bfloat16(), rand(T, E), rand(T, D).bfloat16()
+    layer.forward(x, logits)
+    want = [t.clone() for t in layer.backward(dout, logits)]
+    layer.forward(x, logits)
+    for n in (1, 40):
+        layer.decode(rand(n, D).bfloat16(), rand(n, E))
+    for t in (layer.dy, layer.dlogits):
+        t.fill_(5)
+    assert all(torch.equal(a, b) for a, b in zip(layer.backward(dout, logits), want))
