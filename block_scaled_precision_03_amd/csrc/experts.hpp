@@ -9,6 +9,9 @@
 // and the rounding of what that leaves, 16 bits of mantissa): rounded to one, it
 // would add as much error as the rounding of out (2.3e-3 instead of 1.7e-3 of
 // the result's norm); the second costs a matrix instruction, which the stream hides.
+// The two parts' products have sums of their own: an infinite weight times the low
+// part is an infinity of either sign, or NaN, beside the high part's infinity (see
+// join_planes).
 //
 // Tokens of an expert beyond 16 make further records of up to 16 of it.
 // experts_up_kernel: a workgroup per (record, tile of W1's rows); one more
@@ -251,16 +254,18 @@ struct ExpertStream {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // acc += the stage's product: the result lane holds weight rows 4 q .. + 3 of
-  // activation row i.
-  __device__ inline void consume(const uint8_t *smem, int sl, uint32_t u, v4f &acc) const {
+  // acc += the stage's product, plane by plane: the result lane holds weight
+  // rows 4 q .. + 3 of activation row i.
+  __device__ inline void consume(const uint8_t *smem, int sl, uint32_t u, v4f (&acc)[PL]) const {
     const uint8_t *st = smem + sl * STAGE;
     const uint8_t *wt = st + W_OFF + 2048 * w + i16 * 128;
     const int ri = i16 & (RC - 1), f = xswz(ri);
     const uint8_t *xt = st + X_OFF + (SHARED ? 0 : w * 1024) + ri * F::XPITCH;
     const uint8_t *sc = st + S_OFF + 256 * w;
     const v4i raw[2] = {lds_read16(wt + ((q ^ kswz(i16)) << 4)), lds_read16(wt + (((q + 4) ^ kswz(i16)) << 4))};
-    v4f part = WF == WF_BLOCK ? (v4f){0.f, 0.f, 0.f, 0.f} : acc;
+    v4f part[PL];
+#pragma unroll
+    for (int p = 0; p < PL; ++p) part[p] = WF == WF_BLOCK ? (v4f){0.f, 0.f, 0.f, 0.f} : acc[p];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int piece = q + 4 * h;
@@ -277,15 +282,29 @@ struct ExpertStream {
 #pragma unroll
         for (int p = 0; p < PL; ++p) {
           const v4i xr = lds_read16(xt + p * XPLANE + (((piece * F::SUB + m) ^ f) << 4));
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, xr), part, 0, 0, 0);
+          part[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, xr), part[p], 0, 0, 0);
         }
       }
     }
-    // one FP32 scale for 128 values of K of all of the tile's rows
-    if constexpr (WF == WF_BLOCK) acc += part * *(const float *)sc;
-    else acc = part;
+#pragma unroll
+    for (int p = 0; p < PL; ++p) {
+      // one FP32 scale for 128 values of K of all of the tile's rows
+      if constexpr (WF == WF_BLOCK) acc[p] += part[p] * *(const float *)sc;
+      else acc[p] = part[p];
+    }
   }
 };
+
+// The sum of the two planes' products.  Where the high plane's is infinite or NaN
+// it stands alone: a high part is zero only where its argument is (or is below
+// FP32's normal range), and has its sign, so that beside infinite weights it gives
+// what the argument itself does.
+__device__ inline v4f join_planes(const v4f (&acc)[2]) {
+  v4f v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = fabsf(acc[0][k]) < __builtin_inff() ? acc[0][k] + acc[1][k] : acc[0][k];
+  return v;
+}
 
 // The tokens of every expert as bits.
 struct ExpertMasks {
@@ -543,7 +562,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
   const int lo = split ? s.w * units / EXP_WAVES : 0, hi = split ? (s.w + 1) * units / EXP_WAVES : units;
 #pragma unroll
   for (int k = 0; k < U - 1; ++k) s.issue(k, lo + k, lo + k < hi);
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
   int sl = 0;
   for (int v = lo; v < hi; ++v) {
     Stream::wait();
@@ -554,13 +573,13 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_up_kernel(ExpertsArgs 
   wait_vmem_le<0>();                           // no DMA into LDS that is used for something else
   if (split) {
     __syncthreads();
-    sm.part[s.w][s.lane] = acc;
+    sm.part[s.w][s.lane] = acc[0];
     __syncthreads();
     if (s.w != 0) return;
 #pragma unroll
-    for (int k = 1; k < EXP_WAVES; ++k) acc += sm.part[k][s.lane];
+    for (int k = 1; k < EXP_WAVES; ++k) acc[0] += sm.part[k][s.lane];
   }
-  if (s.i16 < rec.n && n0 + c < p.N1) store_h(p, rec.base + s.i16, n0 + c, acc * chan);
+  if (s.i16 < rec.n && n0 + c < p.N1) store_h(p, rec.base + s.i16, n0 + c, acc[0] * chan);
 }
 
 // TM: the most tokens (the sums' rows).
@@ -610,7 +629,7 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
   if (lo < hi) enter(ia);
 #pragma unroll
   for (int k = 0; k < U - 1; ++k) issue(k);
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  v4f acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   int sl = 0;
   for (int v = lo; v < hi; ++v) {
     Stream::wait();
@@ -621,12 +640,13 @@ __global__ __launch_bounds__(64 * EXP_WAVES) void experts_down_kernel(ExpertsArg
       const uint8_t *st = ring + sl * Stream::STAGE;
       const int t = *(const int32_t *)(st + Stream::P_OFF + (SHARED ? 0 : 256 * s.w) + 8 * s.i16);
       const float share = *(const float *)(st + Stream::P_OFF + (SHARED ? 0 : 256 * s.w) + 8 * s.i16 + 4);
-      if constexpr (WF == WF_INT8) acc *= *(const v4f *)(st + Stream::S_OFF + 256 * s.w + 16 * s.q);
+      v4f y = join_planes(acc);
+      if constexpr (WF == WF_INT8) y *= *(const v4f *)(st + Stream::S_OFF + 256 * s.w + 16 * s.q);
       if (s.i16 < recs[ca].n) {
         v4f *sum = (v4f *)&sums[SHARED ? 0 : s.w][t][(SHARED ? 16 * s.w : 0) + 4 * s.q];
-        *sum += acc * share;
+        *sum += y * share;
       }
-      acc = (v4f){0.f, 0.f, 0.f, 0.f};
+      acc[0] = acc[1] = (v4f){0.f, 0.f, 0.f, 0.f};
       cu = 0;
       ++ca;
     }

@@ -303,3 +303,57 @@ def test_weights_past_4_gib(fmt):
     one.d.update(w1=w1, w2=w2, s1=s1, s2=s2, ids=torch.full((T, k), E - 1, dtype=torch.int32, device=DEV))
     one.E = E
     assert torch.equal(one.run(), want)
+
+
+INFINITE = {"bf16": (0x7F80, 0xFF80), "e5m2": (0x7C, 0xFC)}        # codes of plus and minus infinity
+
+
+@pytest.mark.parametrize("name", sorted(INFINITE))
+@pytest.mark.parametrize("T,E,k,F", [(1, 5, 2, 96), (2, 4, 3, 2592), (6, 3, 2, 96), (40, 6, 4, 2592)])
+@pytest.mark.parametrize("a", [R.ACT_NONE, R.ACT_RELU, R.ACT_SWIGLU])
+def test_infinite_weights_of_the_second_product(name, T, E, k, F, a):
+    """Columns with one infinity, with two (of both signs or not), and without:
+    infinite with the argument's sign, NaN where infinities of both signs meet or one
+    meets a zero, and the others as they were."""
+    fmt = R.FORMATS[name]
+    c = Case(fmt, T, E, k, 96, F, a=a, seed=T)
+    plus, minus = (dev(np.array([v]).astype(c.c2.dtype)).view(c.d["w2"].dtype) for v in INFINITE[name])
+    v2 = c.v2.copy()
+    for d, marks in ((3, ((5, 1),)), (17, ((F - 1, -1),)), (40, ((7, 1), (60, 1))), (41, ((0, 1), (33, -1))), (95, ((64, -1), (65, -1)))):
+        for f, sign in marks:
+            c.d["w2"][:, d, f] = plus if sign > 0 else minus
+            v2[:, d, f] = sign * np.inf
+    got = c.run().float().cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        want, _ = R.experts(c.x, c.ids, c.w, c.v1, v2, a, c.r)
+        clean, tol = R.experts(c.x, c.ids, c.w, c.v1, c.v2, a, c.r)
+    hot = ~np.isfinite(want)
+    assert hot.any() and np.array_equal(got[hot], want[hot], equal_nan=True)
+    assert (np.abs(got - clean) <= tol)[~hot].all()
+
+
+@pytest.mark.parametrize("name", sorted(INFINITE))
+@pytest.mark.parametrize("T", [1, 5])
+def test_infinite_weights_and_arguments_without_a_low_part(name, T):
+    """Arguments that one BF16 holds exactly."""
+    fmt = R.FORMATS[name]
+    c = Case(fmt, T, 1, 1, 96, 96, ids=np.zeros((T, 1)), a=R.ACT_NONE, residual=False)
+    one = 0x3F80 if fmt == R.BF16 else 0x3C
+    minus = INFINITE[name][1] - (1 << 16 if fmt == R.BF16 else 0)
+    for n in ("w1", "w2"):
+        c.d[n].zero_()
+    if fmt != R.BF16:
+        c.d["s1"].fill_(127)
+        c.d["s2"].fill_(127)
+    c.d["x"].zero_()
+    c.d["w"].fill_(1.0)
+    i = torch.arange(96, device=DEV)
+    c.d["w1"][0, i, i] = one                   # h = x
+    for d, f, code in ((10, 0, INFINITE[name][0]), (11, 1, minus), (12, 2, minus), (13, 3, one)):
+        c.d["w2"][0, d, f] = code
+    c.d["x"][0, 0], c.d["x"][0, 1], c.d["x"][0, 2], c.d["x"][0, 3] = 1.0, -2.0, 3e38, -2.0
+    got = c.run().float()
+    inf = float("inf")
+    assert got[0, 10] == inf and got[0, 11] == inf and got[0, 12] == -inf and got[0, 13] == -2.0
+    # zeros beside infinite weights are NaN, whoever's token they are
+    assert torch.isnan(got[1:, 10:13]).all() and (got[:, :10] == 0).all() and (got[:, 14:] == 0).all()
