@@ -19,16 +19,17 @@ struct ResidualGradArgs {
   int64_t M, N, No, rows;          // rows per part
 };
 
-// act'(z).
+// act'(z) of the activations that have one everywhere.
 //   GELU (tanh form): z s(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
 //     s + z s (1 - s) 2u',  u' = sqrt(2/pi) (1 + 0.134145 z^2)
 //   SiLU: s + z s (1 - s)
+//   (ReLU's gradient is dD where z > 0 and 0 elsewhere, chosen, not multiplied: a
+//   dead unit has none even where dD is infinite or NaN.)
 // 1 - s is formed as the logistic function of the negated argument, which
 // keeps its leading bits where s is near 1, and z s (1 - s) as 0 where it
 // vanishes (|z| large), not as infinity times zero.
 template <int ACT>
 __device__ inline float act_slope(float z) {
-  if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if constexpr (ACT == ACT_GELU_TANH) {
     const float c = fminf(fmaxf(z, -16.0f), 16.0f);        // beyond: exactly 0 or 1
     const float u2 = 1.5957691216057308f * fmaf(0.044715f * c, c * c, c);
@@ -123,7 +124,10 @@ __global__ __launch_bounds__(64 * W) void residual_grad_kernel(ResidualGradArgs 
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k) g[k] = ACT == ACT_NONE ? d[i][k] : d[i][k] * act_slope<ACT>(z[i][k]);
+          for (int k = 0; k < V; ++k) {
+            if constexpr (ACT == ACT_RELU) g[k] = z[i][k] > 0.0f ? d[i][k] : 0.0f;
+            else g[k] = ACT == ACT_NONE ? d[i][k] : d[i][k] * act_slope<ACT>(z[i][k]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) sum[k] += g[k];

@@ -754,9 +754,9 @@ int moe_experts_validate(int fmt, const void *x, const int32_t *ids, const float
  * workspace, workspace_bytes  for dbias: 16-byte aligned device memory of at
  *         least mxgemm_residual_backward_workspace_bytes(M, N) bytes (0 for few
  *         rows), free once the call's work is done.
- * dD, z, dz 16-byte aligned; M, N < 2^31.  ReLU's slope at 0 is 0.  At most two
- * kernels.  N = 0: no-op.  Neither dz nor dbias, or a small workspace, is
- * MXG_ERR_INVALID_ARG.
+ * dD, z, dz 16-byte aligned; M, N < 2^31.  ReLU: dz = dD where z > 0, else 0
+ * (whatever dD is).  At most two kernels.  N = 0: no-op.  Neither dz nor dbias,
+ * or a small workspace, is MXG_ERR_INVALID_ARG.
  */
 int mxgemm_run_residual(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
                         void *D, int64_t M, int64_t N, int64_t K, const void *bias, int activation,

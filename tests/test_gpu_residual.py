@@ -412,3 +412,20 @@ def test_block_forward_and_gradient():
     _, slip, _, btol = R.gradient(d, z, R.ACT_GELU)
     assert ((dz.double() - leaf.grad).abs() <= (leaf.grad.abs() + slip) * R.HALF_BF16 + slip).all()
     assert ((db.double() - b.grad).abs() <= btol).all()
+
+
+@pytest.mark.parametrize("M,N", [(4, 8), (3, 1030), (300, 520)])
+def test_gradient_of_dead_units(M, N):
+    """ReLU: no gradient where z is not positive, whatever arrives there."""
+    m = _mx()
+    inf, nan = float("inf"), float("nan")
+    d = torch.tensor([inf, -inf, nan, 2.0], device=DEV).repeat(M, N // 4 + 1)[:, :N].to(b16).contiguous()
+    z = torch.tensor([-1.0, 0.0, -3.0, -4.0, 5.0, 6.0, 7.0, 8.0], device=DEV).repeat(M, N // 8 + 1)[:, :N].to(b16).contiguous()
+    want = torch.where(z > 0, d, torch.zeros_like(d))
+    dz, db = torch.empty(M, N, dtype=b16, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.empty(m.residual_backward_workspace_bytes(M, N) + 16, dtype=torch.uint8, device=DEV)
+    m.residual_backward(R.ACT_RELU, d, z, dz, db, M, N, workspace=ws)
+    assert torch.equal(dz.nan_to_num(-9), want.nan_to_num(-9)) and torch.equal(dz.isnan(), want.isnan())
+    # sums of equal values, multiples of 2 below 2^24: exact
+    sums = M * want[0].float()
+    assert torch.equal(db.nan_to_num(-9), sums.nan_to_num(-9)) and torch.equal(db.isnan(), sums.isnan())
