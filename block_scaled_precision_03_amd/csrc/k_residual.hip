@@ -76,9 +76,9 @@ extern "C" int mxgemm_residual_backward(int activation, const void *dD, const vo
                                         int64_t N, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
   const int v = mxgemm_residual_backward_validate(activation, dD, z, dz, dbias, M, N, workspace, workspace_bytes);
   if (v != MXG_OK || N == 0) return v;
-  const unsigned sums = (unsigned)cdiv(N, 64);
+  const dim3 sums = flat_grid(cdiv(N, 64));
   if (M == 0) {
-    if (dbias) hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(64 * CS_WAVES), 0, stream, nullptr, dbias, N, 0);
+    if (dbias) hipLaunchKernelGGL(column_sums_kernel, sums, dim3(64 * CS_WAVES), 0, stream, nullptr, dbias, N, 0);
     return launch_status();
   }
   const GradShape s = grad_shape(M, N);
@@ -91,9 +91,11 @@ extern "C" int mxgemm_residual_backward(int activation, const void *dD, const vo
   a.N = N;
   a.No = activation == MXG_ACT_SWIGLU ? N / 2 : N;
   a.rows = s.rows;
-  hipLaunchKernelGGL((s.few ? pick_grad<RG_FEW_V, 16>(activation) : pick_grad<8, 4>(activation)),
-                     dim3((unsigned)s.stripes, (unsigned)s.parts), dim3(s.few ? 1024 : 256), 0, stream, a);
+  if (s.few)
+    hipLaunchKernelGGL((pick_grad<RG_FEW_V, RG_FEW_WAVES>(activation)), flat_grid(s.stripes), dim3(64 * RG_FEW_WAVES), 0, stream, a);
+  else
+    hipLaunchKernelGGL((pick_grad<8, 4>(activation)), dim3((unsigned)s.stripes, (unsigned)s.parts), dim3(256), 0, stream, a);
   if (dbias && s.parts > 1)
-    hipLaunchKernelGGL(column_sums_kernel, dim3(sums), dim3(64 * CS_WAVES), 0, stream, (const float *)workspace, dbias, N, (int)s.parts);
+    hipLaunchKernelGGL(column_sums_kernel, sums, dim3(64 * CS_WAVES), 0, stream, (const float *)workspace, dbias, N, (int)s.parts);
   return launch_status();
 }

@@ -84,8 +84,9 @@ struct RowPiece {
 // V columns of z per lane, RG_ROWS rows at a time (their loads in flight
 // together); block (x, y): columns 64 V x .., the rows of part y, row r of them to
 // wave r % W.  Many rows: V 8, four waves, parts that a second kernel sums; few:
-// V 2, sixteen waves and one part, one kernel (V 4: 129 x 5002 11.6 us, 7.2).
-constexpr int RG_ROWS = 4, RG_FEW_V = 2;
+// V 2, sixteen waves and one part, one kernel (V 4: 129 x 5002 11.6 us, 7.2), whose
+// grid is folded (flat_grid): 2^29 columns would make 2^32 work-items in one dimension.
+constexpr int RG_ROWS = 4, RG_FEW_V = 2, RG_FEW_WAVES = 16;
 
 template <int ACT, int V, int W>
 __global__ __launch_bounds__(64 * W) void residual_grad_kernel(ResidualGradArgs p) {
@@ -93,9 +94,9 @@ __global__ __launch_bounds__(64 * W) void residual_grad_kernel(ResidualGradArgs 
   constexpr int DV = GATED ? V / 2 : V, COLS = 64 * V;
   __shared__ float sums[W][COLS];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * COLS + lane * V, room = p.N - c;
+  const int64_t c0 = (W == RG_FEW_WAVES ? flat_block() : (int64_t)blockIdx.x) * COLS, c = c0 + lane * V, room = p.N - c;
   const int64_t cd = GATED ? c / 2 : c, roomd = GATED ? room / 2 : room;
-  const int64_t m0 = (int64_t)blockIdx.y * p.rows, m1 = min(p.M, m0 + p.rows);
+  const int64_t part = W == RG_FEW_WAVES ? 0 : blockIdx.y, m0 = part * p.rows, m1 = min(p.M, m0 + p.rows);
   float sum[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) sum[k] = 0.0f;
@@ -140,12 +141,12 @@ __global__ __launch_bounds__(64 * W) void residual_grad_kernel(ResidualGradArgs 
   for (int k = 0; k < V; ++k) sums[w][lane * V + k] = sum[k];
   __syncthreads();
   for (int i = threadIdx.x; i < COLS; i += 64 * W) {
-    const int64_t col = (int64_t)blockIdx.x * COLS + i;
+    const int64_t col = c0 + i;
     if (col >= p.N) continue;
     float t = sums[0][i];
 #pragma unroll
     for (int k = 1; k < W; ++k) t += sums[k][i];
-    p.part[(int64_t)blockIdx.y * p.N + col] = t;
+    p.part[part * p.N + col] = t;
   }
 }
 
@@ -156,7 +157,7 @@ constexpr int CS_WAVES = 16;
 __global__ __launch_bounds__(64 * CS_WAVES) void column_sums_kernel(const float *part, float *out, int64_t N, int parts) {
   __shared__ float sums[CS_WAVES][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t n = flat_block() * 64 + lane;
   float s = 0.0f;
   if (n < N) {
     for (int k0 = w; k0 < parts; k0 += 8 * CS_WAVES) {

@@ -429,3 +429,21 @@ def test_gradient_of_dead_units(M, N):
     # sums of equal values, multiples of 2 below 2^24: exact
     sums = M * want[0].float()
     assert torch.equal(db.nan_to_num(-9), sums.nan_to_num(-9)) and torch.equal(db.isnan(), sums.isnan())
+
+
+def test_gradient_of_very_long_rows():
+    """More workgroups than one dimension of a grid holds: 2^29 columns and
+    some, and the zeros of no rows."""
+    m = _mx()
+    N = (1 << 29) + 130
+    d = torch.ones(1, N, dtype=b16, device=DEV)
+    z = torch.full((1, N), -1.0, dtype=b16, device=DEV)
+    at = torch.tensor([0, 1, 127, 128, (1 << 27) - 1, 1 << 27, 1 << 28, (1 << 29) - 1, 1 << 29, N - 3, N - 1], device=DEV)
+    z[0, at] = 1.0
+    dz, db = torch.full((1, N), 7.0, dtype=b16, device=DEV), torch.full((N,), 7.0, device=DEV)
+    assert m.residual_backward_workspace_bytes(1, N) == 0
+    m.residual_backward(R.ACT_RELU, d, z, dz, db, 1, N)
+    assert (dz[0, at] == 1).all() and (db[at] == 1).all()
+    assert int((dz != 0).sum()) == at.numel() and int((db != 0).sum()) == at.numel()
+    m.residual_backward(R.ACT_RELU, None, None, None, db, 0, N)
+    assert int((db != 0).sum()) == 0
