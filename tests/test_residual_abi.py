@@ -88,3 +88,12 @@ def test_gradient_against_differences(a):
             # (below 10 |d u|), and by the sums' rounding over h
             assert abs(float(diff - dz[i, j])) <= 10 * h * h * 20 + 1e-9
     assert torch.equal(dbias, dz.sum(0))
+
+
+@pytest.mark.parametrize("fmt", [0, 4, 16, 32])
+def test_forward_most_columns(fmt):
+    m = _mx()
+    most = lambda N, **kw: m.validate_residual(fmt, fmt, 0, P, P, P, P, P, 64, N, 256, **kw)
+    for kw in (dict(residual=Q), dict(z=Q)):
+        assert most(4194304, **kw) == 0 and most(4194305, **kw) == -2
+    assert most(4194305) == 0                  # neither: as run_fused
