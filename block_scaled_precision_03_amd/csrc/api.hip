@@ -167,37 +167,43 @@ extern "C" int mxgemm_validate(int fmtA, int fmtB, int layout, const void *A, co
   return MXG_OK;
 }
 
-// Kernel choice of the residual epilogue: those of mxgemm_dense_variant, and
-// the kernels for few rows or columns (rows.hpp) by estimated times from static
-// shapes, fitted to 250 calls of 1 .. 400 rows (N 128 .. 16000, K 256 .. 15360, MXFP8
-// and MXFP4, plain and preshuffled B, cold weights), every kernel timed on each:
-// 1 % over the fastest on average, over 14 % in 5 of them, at most 27 %.  Both sides where the
-// choice turns, in us (8 x 16, 16 x 16, 32 x 32, 64 x 32, 64 x 64 tiles; the 64 x 64 kernel of
-// small.hpp): 16 x 8192 x 8192 FP8 25, 18.4, 16.5, 17.1, 24.7; 64; 17 x 2796 x 1792 7.9, 7.6, 5.6,
-// 6.5, 8.2; 14.7; 44 x 8461 x 2048 -, 27, 17.1, 14.5, 10.9; 25.9; 4 x 14096 x 256 FP4 6.0, 10.6, 6.7,
-// 7.4, 4.9; 4.0.
+// Kernel choice of the residual epilogue, every kernel by one kind of
+// estimate from static shapes: the tiles of ROWS_TILES (rows.hpp), the 64 x 64 kernel
+// (small.hpp) and the 256 x 256 one with its epilogue between two tiles.  Fitted to
+// 1488 calls of 1 .. 16000 rows (N 96 .. 16000, K 256 .. 14336, MXFP8 and MXFP4, plain
+// and preshuffled B, no activation and GELU, cold weights), every kernel timed on each
+// (the tiles of up to 32 rows not above 64, 128 and 1024 rows): 0.6 % over the fastest on
+// average, over 14 % in 13 of them, at most 34 %; fitted to two thirds of them, 0.6 %
+// on the others, over 14 % in 1 of 496.  Both sides where the choice turns, in us (best
+// of ROWS_TILES; 64 x 64; 256 x 256): MXFP8 233 x 5186 x 2432 22.8, 40.7, 41.5; 731 x
+// 1472 x 512 12.4, 12.8, 20.8; 794 x 2496 x 7680 54, 135, 109; 1517 x 2304 x 768 25.9, 31.7,
+// 25.3; MXFP4, preshuffled, 1991 x 1408 x 768 17.5, 12.3, 19.7; 541 x 4800 x 2304 26.3, 26.4,
+// 29.0; 2384 x 2944 x 1280 48, 33, 24.
 namespace {
-// The tile of the kernel for few rows that is fastest, -1: another kernel.
-int rows_tile(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  if (layout != MXG_NT || M <= 0 || N <= 0 || K < 128 || fmtA == MXG_INT8) return -1;
-  // more rows: only where 64 x 64 tiles leave compute units idle (with K split and
-  // with the 64 x 64 kernel, us: 635 x 194 x 8704 MXFP8 9.8, 75; 2048 x 194 x 4096 9.4, 45; 8000 x
-  // 100 x 512 6.4, 7.8)
-  if (M > 512 && cdiv(M, SBM) * cdiv(N, SBN) > cu_count()) return -1;
+enum : int { RES_TILE64 = ROWS_TILE_COUNT, RES_TILE256 };     // 0 .. ROWS_TILE_COUNT - 1: ROWS_TILES
+int residual_kernel(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
+  if (layout != MXG_NT || M <= 0 || N <= 0 || K < 128) return RES_TILE256;
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0, fp4 = fmtA == MXG_MXFP4_E2M1;
   const double cus = cu_count(), nst = (double)(K / 128), kb = fp4 ? 0.5 * K : (double)K;
   const double bytes = (double)N * kb + (double)M * kb + 4.0 * (double)M * (double)N;
-  // start; a tile's own time; a compute unit's operand bytes and all memory's per us
+  // ROWS_TILES: start; a tile's own time; a compute unit's operand bytes and all memory's per us
   struct Model { double t0, tile, rate, mem; };
   const Model model[2][ROWS_TILE_COUNT] = {
-      {{2.15, 1.46, 43.2e3, 5.45e6}, {1.52, 2.41, 50.3e3, 4.65e6}, {1.03, 2.92, 48.3e3, 3.73e6}, {1.31, 3.24, 42.5e3, 3.46e6}, {0.0, 4.97, 42.0e3, 2.82e6}},
-      {{2.39, 1.24, 42.5e3, 5.24e6}, {1.61, 2.47, 65.2e3, 4.36e6}, {1.14, 3.05, 53.7e3, 3.98e6}, {1.34, 3.63, 49.2e3, 3.27e6}, {0.0, 5.61, 45.6e3, 3.29e6}}};
-  // the 64 x 64 kernel as timed there; the 256 x 256 one as mxgemm_dense_variant has it
-  const double t64[2][2][3] = {{{3.77, 0.943, 1.89}, {3.82, 0.555, 2.48}}, {{3.73, 0.523, 2.82}, {4.13, 0.340, 2.89}}};
-  const double *s = t64[psb][fp4], n64 = (double)(cdiv(M, SBM) * cdiv(N, SBN));
-  double least = s[0] + std::ceil(n64 / cus) * s[1] * nst + s[2] * n64 / cus;
-  least = std::min(least, 6.0 + std::ceil((double)(cdiv(M, DBM) * cdiv(N, DBN)) / cus) * 1.3 * nst);
-  int best = -1;
+      {{2.25, 1.20, 44.0e3, 4.29e6}, {1.39, 2.52, 58.6e3, 3.77e6}, {1.61, 2.31, 51.6e3, 3.59e6}, {1.40, 3.19, 49.2e3, 3.01e6}, {0.23, 5.17, 47.9e3, 3.06e6}},
+      {{2.15, 1.43, 46.0e3, 4.83e6}, {1.40, 2.57, 61.8e3, 3.96e6}, {1.57, 2.54, 58.7e3, 4.00e6}, {1.41, 3.37, 54.3e3, 3.33e6}, {0.0, 5.59, 52.6e3, 2.63e6}}};
+  // the others: start; a K step's time in a round of tiles; a tile's (a round's) own time
+  const double t64[2][2][3] = {{{3.58, 0.95, 1.73}, {3.63, 0.592, 1.07}}, {{3.34, 0.623, 1.73}, {3.60, 0.379, 1.21}}};
+  const double t256[2][2][3] = {{{3.51, 1.70, 13.62}, {2.45, 0.77, 14.86}}, {{0.65, 1.29, 18.82}, {0.0, 0.78, 17.92}}};
+  const double *s = t64[psb][fp4], *b = t256[psb][fp4], n64 = (double)(cdiv(M, SBM) * cdiv(N, SBN));
+  double least = b[0] + std::ceil((double)(cdiv(M, DBM) * cdiv(N, DBN)) / cus) * (b[1] * nst + b[2]);
+  int best = RES_TILE256;
+  auto take = [&](int kernel, double us) {
+    if (us < least) {
+      least = us;
+      best = kernel;
+    }
+  };
+  take(RES_TILE64, s[0] + std::ceil(n64 / cus) * s[1] * nst + s[2] * n64 / cus);
   for (int i = 0; i < ROWS_TILE_COUNT; ++i) {
     const RowsTile &t = ROWS_TILES[i];
     const Model &m = model[psb][i];
@@ -205,18 +211,16 @@ int rows_tile(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
     const double n = (double)(tm * cdiv(N, t.cols)), ops = (std::min((double)t.rows, (double)M / tm) + t.cols) * kb;
     // tiles per compute unit: whole rounds where one fills it
     const double load = t.per_cu > 1 ? std::max(1.0, n / cus) : std::ceil(n / cus);
-    const double us = m.t0 + std::max(load * (m.tile + ops / m.rate), bytes / m.mem);
-    if (us < least) {
-      least = us;
-      best = i;
-    }
+    take(i, m.t0 + std::max(load * (m.tile + ops / m.rate), bytes / m.mem));
   }
   return best;
 }
 }  // namespace
 
 extern "C" int mxgemm_residual_variant(int fmtA, int fmtB, int layout, int64_t M, int64_t N, int64_t K) {
-  return rows_tile(fmtA, fmtB, layout, M, N, K) >= 0 ? MXG_DENSE_ROWS : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+  if (fmtA == MXG_INT8) return mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K);
+  const int k = residual_kernel(fmtA, fmtB, layout, M, N, K);
+  return k == RES_TILE256 ? MXG_DENSE_TILE256 : k == RES_TILE64 ? MXG_DENSE_TILE64 : MXG_DENSE_ROWS;
 }
 
 namespace {
@@ -256,7 +260,7 @@ __global__ void bias_act_fill_kernel(uint16_t *D, int64_t M, int64_t N, const ui
 
 int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, const void *B, const void *sB,
               void *D, int64_t M, int64_t N, int64_t K, const void *bias, int act, const void *residual, void *z,
-              bool few_rows, hipStream_t stream) {
+              bool res, hipStream_t stream) {
   if (fmtA == MXG_INT8) return int8_run(A, sA, B, sB, D, M, N, K, bias, act, residual, z, stream);
   const int fuse = residual != nullptr || z != nullptr        ? (act != MXG_ACT_NONE ? FUSE_RES_ACT : FUSE_RES)
                    : bias != nullptr || act != MXG_ACT_NONE ? FUSE_ACT
@@ -274,9 +278,10 @@ int run_dense(int fmtA, int fmtB, int layout, const void *A, const void *sA, con
   }
   const bool psb = (fmtB & MXG_PRESHUFFLED) != 0;
   const FmtInfo fa = fmt_info(fmtA), fb = fmt_info(fmtB & ~MXG_PRESHUFFLED);
-  const int tile = few_rows ? rows_tile(fmtA, fmtB, layout, M, N, K) : -1;
-  const bool rows = tile >= 0;
-  const bool small = !rows && mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64;
+  const int tile = res ? residual_kernel(fmtA, fmtB, layout, M, N, K)
+                   : mxgemm_dense_variant(fmtA, fmtB, layout, M, N, K) == MXG_DENSE_TILE64 ? RES_TILE64
+                                                                                        : RES_TILE256;
+  const bool rows = tile < ROWS_TILE_COUNT, small = tile == RES_TILE64;
   dense_fn fn = rows    ? pick_rows(fa.elem, fb.elem, fa.mx, psb, tile)
                 : small ? pick_small(fa.elem, fb.elem, fa.mx, psb, fuse)
                         : pick_dense(fa.elem, fb.elem, fa.mx, layout, psb, fuse);

@@ -28,7 +28,7 @@ def _mx():
 @pytest.mark.parametrize("name", sorted(PAIRS))
 @pytest.mark.parametrize("psb", [False, True])
 @pytest.mark.parametrize("M,N,K,kernel", [(3, 70, 1024, "DENSE_ROWS"), (25, 1026, 2048, "DENSE_ROWS"), (60, 8194, 2048, "DENSE_ROWS"),
-                                          (4, 40000, 256, "DENSE_TILE64"), (2148, 2362, 512, "DENSE_TILE256"),
+                                          (4, 40000, 256, "DENSE_TILE64"), (2148, 2362, 1024, "DENSE_TILE256"),
                                           (2148, 2304, 768, "DENSE_TILE256")])
 def test_every_pair_on_every_kernel(name, psb, M, N, K, kernel):
     m = _mx()
@@ -44,7 +44,7 @@ def test_every_pair_on_every_kernel(name, psb, M, N, K, kernel):
 @pytest.mark.parametrize("bias,residual,z", [(False, True, False), (False, False, True), (False, True, True)])
 def test_every_part_alone(name, psb, bias, residual, z):
     T.Case(name, 37, 259, 512, a=R.ACT_SILU, bias=bias, residual=residual, z=z, psb=psb).check()
-    T.Case(name, 2049, 2307, 512, a=R.ACT_NONE, bias=bias, residual=residual, z=z, psb=psb).check()
+    T.Case(name, 2049, 2307, 1024, a=R.ACT_NONE, bias=bias, residual=residual, z=z, psb=psb).check()
 
 
 @pytest.mark.parametrize("name", ["mx44", "mx55", "fp4", "tw44"])

@@ -97,3 +97,19 @@ def test_forward_most_columns(fmt):
     for kw in (dict(residual=Q), dict(z=Q)):
         assert most(4194304, **kw) == 0 and most(4194305, **kw) == -2
     assert most(4194305) == 0                  # neither: as run_fused
+
+
+# (format, preshuffled B, M, N, K, the kernel that was fastest, its us, the others' least us); the measured
+# times of the kernel families on 256 compute units, differences of 15 % and more
+FASTEST = [(0, False, 1857, 688, 7936, "ROWS", 50, 119), (4, True, 787, 1443, 12544, "ROWS", 40, 83), (0, False, 794, 2496, 7680, "ROWS", 54, 109),
+           (0, True, 2243, 872, 12800, "ROWS", 60, 136), (4, False, 824, 1984, 2048, "ROWS", 16, 27), (0, False, 233, 5186, 2432, "ROWS", 23, 41),
+           (4, True, 632, 3520, 512, "TILE64", 11, 20), (4, True, 295, 7104, 1024, "TILE64", 18, 21), (4, True, 1991, 1408, 768, "TILE64", 12, 18),
+           (0, False, 724, 5499, 256, "TILE64", 21, 34), (0, True, 1690, 6848, 1536, "TILE256", 35, 97), (4, False, 2579, 2752, 512, "TILE256", 19, 28)]
+
+
+@pytest.mark.parametrize("fmt,psb,M,N,K,kernel,us,others", FASTEST)
+def test_forward_kernel_choice(fmt, psb, M, N, K, kernel, us, others):
+    """One estimate for all kernels: the choice is the kernel that runs."""
+    m = _mx()
+    assert 1.15 * us < others
+    assert m.residual_variant(fmt, fmt | (m.PRESHUFFLED if psb else 0), m.NT, M, N, K) == getattr(m, "DENSE_" + kernel)
