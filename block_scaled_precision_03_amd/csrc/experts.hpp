@@ -27,14 +27,15 @@
 //     of out), the list split over the waves, whose sums meet at the end.
 //   shared: 64 rows, 16 per wave, one ring; the activations of a stage, up to 16
 //     rows of them, are brought once for all four waves.
-// Both sides for one token, the kernels' us, private and shared: 4 of 1024 x 512 INT8
-// 5.0 + 5.5, 7.5 + 6.8; 8 of 7168 x 2304 MXFP4 33 + 21, 34 + 24.
+// Both sides for one token, the call's us (copies of the weights in turn, none of
+// them cached), private and shared: 4 of 1024 x 512 INT8 10.2, 13.5; 8 of 7168 x 2304
+// MXFP4 53.7, 61.8.
 //
 // Bound by memory where the experts are large: 16 tokens, 8 each, 64 experts of
-// 7168 x 2304 INT8, SwiGLU 493 us, 5.7 TB/s of weights (records of up to 8 tokens; a fifth wave
-// that does the loads: 428 + 255 us in place of 319 + 200); 1 token, 8 of them
-// in MXFP4 53 us, 3.7 TB/s.  By the two kernels' starts where they are small (1 token, 4
-// of 1024 x 512: 9.3 us).
+// 7168 x 2304 INT8, SwiGLU 487 to 493 us, 5.7 TB/s of weights (records of up to 8 tokens;
+// a fifth wave that does the loads made the two kernels a third and a quarter
+// slower); 1 token, 8 of them in MXFP4 53 us, 4.0 TB/s.  By the two kernels' starts
+// where they are small (1 token, 4 of 1024 x 512: 9.7 us).
 #pragma once
 #include "small.hpp"
 
@@ -137,7 +138,10 @@ __device__ inline bf16x8_t weight_values(const v4i &raw, int m, float scale) {
 //     weight piece p are pieces SUB p ..; each read's 16-lane phases (see kswz)
 //     land on 16 different 16-byte bank groups: rows {0-3, 12-15} at one value of
 //     q and {4-11} at the next, so the set of xswz of the first eight must not change
-//     when it is shifted by the XOR of their pieces (1, 2 or 4).
+//     when it is shifted by the XOR of their pieces (1, 2 or 4).  That is not so with
+//     8 rows of 256 bytes (records of up to 8 tokens of INT8, E4M3, E5M2 and block
+//     weights), where both halves of a phase are the same 8 rows on the same 8 groups,
+//     two accesses each: 0.4 of the LDS cycles of kernels that memory bounds.
 //   S: the aligned dwords around a row's E8M0 scales of the unit (2 per row,
 //     E2M1 4); the channel scales (INT8, DOWN); the unit's block scale.
 template <int WF, int PL, int ROWS, bool DOWN, int U>

@@ -142,9 +142,10 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   // where 64 rows would leave compute units idle or K is long enough for
   // four times as many starts, each of which reads the choice (P slots); else 64
   // rows.  Fitted to 189 calls with both timed, weights cold: 0.2 % over the faster
-  // one on average, at most 9 %.  Both sides, 16 and 64 rows, in us of the call: MXFP8, 1 token,
-  // 8 of 7168 x 2304 84.6, 105.5; 4 of 1024 x 512 INT8 9.3, 11.0; 2 of 2048 x 8192 INT8 32.8, 29.5;
-  // 2 tokens, 16 of 2048 x 768 INT8 27.6, 24.5.
+  // one on average, at most 9 %.  Both sides, 16 and 64 rows, in us of the call (here and
+  // below: copies of the weights in turn, none of them cached): MXFP8, 1 token, 8 of
+  // 7168 x 2304 95.7, 112; 4 of 1024 x 512 INT8 10.1, 11.4; 2 of 2048 x 8192 INT8 33.2, 30.1;
+  // 2 tokens, 16 of 2048 x 768 INT8 29.6, 27.8.
   const int64_t up_units = cdiv(f.row_bytes(D), 128);
   a.split_k = few && (4 * live * cdiv(a.N1, 64) < 3 * cu_count() || 2 * up_units >= 32 + 3 * P);
   a.up_tiles = (int)cdiv(a.N1, a.split_k ? 16 : 64);
@@ -153,19 +154,19 @@ extern "C" int moe_experts(int fmt, const void *x, const int32_t *ids, const flo
   // split over several workgroups (at most EXP_SPLIT_BLOCKS in all, which bounds
   // their sums).  A split costs its share of the last workgroup's additions, about
   // 0.2 + 0.006 T us, and saves units: 0.8 us each, shared, and a quarter private
-  // (second kernel, in us: 37 tokens, 24 experts of 2080 x 1440 MXFP8, 1, 8 and 15
-  // splits: 174, 34.3, 27.6; 64 tokens, 8 of 4096 x 4096: 1 and 8: 180, 43.4; 16
-  // tokens, 64 of 7168 x 2304 INT8, 2 and 4: 314, 222; a short list, 1 token, 4 of
-  // 1024 x 512 INT8, 1 and 2: 5.5, 6.3).
+  // (the call, in us: 37 tokens, 24 experts of 2080 x 1440 MXFP8, 1, 8 and 15
+  // splits: 224, 82, 77; 64 tokens, 8 of 4096 x 4096 block FP8, 1 and 8: 252, 117; 16
+  // tokens, 64 of 7168 x 2304 INT8, 1, 2 and 4: 860, 596, 501; a short list, 1 token, 4
+  // of 1024 x 512 INT8, 1 and 2: 10.2, 10.7).
   const double units = (double)live * (double)cdiv(f.row_bytes(F), 128) / (few ? EXP_WAVES : 1);
   const double best = std::sqrt(units * 0.8 / (0.2 + 0.006 * (double)T));
   a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(EXP_SPLIT_BLOCKS / a.down_tiles, (int64_t)best));
   if (few && units < 24.0) a.splits = 1;
   // Up to 5 tokens per expert that has any: records of 8, whose smaller
   // stages leave room for more of them in flight; else 16 (an expert of more
-  // tokens than that is read again).  Both kernels with 8 and 16, in us: 16 tokens,
-  // 2 per expert, 64 of 7168 x 2304 INT8 545, 564; 37 tokens, 7 per expert, 24 of 2080
-  // x 1440 MXFP8 70, 60; 64 tokens, 16 per expert, 8 of 4096 x 4096 147, 107.
+  // tokens than that is read again).  Both sides, 8 and 16, in us of the call: 16 tokens,
+  // 2 per expert, 64 of 7168 x 2304 INT8 494, 498; 37 tokens, 7 per expert, 24 of 2080
+  // x 1440 MXFP8 83, 77; 64 tokens, 16 per expert, 8 of 4096 x 4096 block FP8 147, 116.
   a.rows = P <= 5 * live ? 8 : EXP_ROWS;
   // records: experts with tokens, and one more per `rows` tokens of an expert
   const int64_t most = live + (P - live) / a.rows;

@@ -703,7 +703,7 @@ enum { MXG_FP8_E4M3_BLOCK = 18 };
  *         moe_experts_workspace_bytes(T, topk, F) bytes, free for other use once
  *         the call's work is done; calls that may run at the same time need one
  *         each.
- * T <= 64 (more: the grouped products), E <= 1024, topk <= 32, D and F <= 131072,
+ * T <= 64 (more: the grouped products, with INT8, BF16 or block weights), E <= 1024, topk <= 32, D and F <= 131072,
  * both multiples of 16 (INT8), 8 (BF16), 32 (MX) or 128 (block): else
  * MXG_ERR_UNSUPPORTED; an unknown enum, null pointer, negative size, E or topk
  * below 1 or a small workspace is MXG_ERR_INVALID_ARG; x, w1, w2, E8M0 scales,
