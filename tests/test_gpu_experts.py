@@ -357,3 +357,13 @@ def test_infinite_weights_and_arguments_without_a_low_part(name, T):
     assert got[0, 10] == inf and got[0, 11] == inf and got[0, 12] == -inf and got[0, 13] == -2.0
     # zeros beside infinite weights are NaN, whoever's token they are
     assert torch.isnan(got[1:, 10:13]).all() and (got[:, :10] == 0).all() and (got[:, 14:] == 0).all()
+
+
+@pytest.mark.parametrize("T,D,F", [(1, 160, 64), (9, 160, 64), (40, 128, 2592)])
+def test_stream_updated_in_place(T, D, F):
+    """x, the residual and out one buffer: a residual stream in place."""
+    c = Case(R.INT8, T, 5, 2, D, F, a=R.ACT_SILU)
+    c.d["r"] = c.d["x"].clone()
+    want = c.run().clone()
+    x = c.d["x"]
+    assert torch.equal(c.run(out=x, residual=x), want)
